@@ -95,6 +95,7 @@ typedef struct {
 enum {
   MUON_OK = 0,
   MUON_WARN_NONFINITE = 1,    /* muon_check_status only: a NaN/Inf reached an update matrix   */
+  MUON_WARN_TOKEN = 2,        /* muon_check_status only: a token id was past the vocabulary     */
   MUON_ERR_INVALID_ARG = -1,  /* bad pointer, size, count, step count or aliasing             */
   MUON_ERR_UNSUPPORTED = -2,  /* no sm_100 device, or a dtype/precision combination not built  */
   MUON_ERR_WORKSPACE = -3,    /* workspace allocation failed (device out of memory)           */
@@ -202,13 +203,115 @@ MUON_API int muon_adamw_step(int count, float* const* params, const void* const*
                              const int64_t* numel, int64_t step, float lr, float beta1, float beta2,
                              float eps, float weight_decay, muon_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Operators that make the gradients which the two steps take: the token embedding and the norm
+ * scales (muon_adamw_step) and the 2-D hidden weights (muon_step), each with the forward pass that
+ * belongs to it.
+ *
+ * Matrices here are row-major with contiguous rows; a *_stride is the distance between rows in
+ * elements, at least the row length. Rows that are multiples of 8 elements, 16-byte aligned, take
+ * the fast paths; any other alignment and width is accepted. Workspaces are the caller's: device
+ * memory, 256-byte aligned, at least as large as the *_workspace call says (that call needs no
+ * device; it returns bytes, or a negative error code), free for other use once the call's work on
+ * the stream is done. These calls allocate nothing, keep nothing between calls and may be captured
+ * into graphs and run concurrently on several streams with workspaces of their own; make a
+ * process's first call on a device outside a capture. Outputs may overlap no other buffer, except
+ * where a call says so. Sums and statistics are fp32, in an order that does not change from run to
+ * run. These launches count in muon_launch_count; muon_profile_read does not time them.
+ * ------------------------------------------------------------------------------------------- */
+
+/*
+ * Token embedding: out[t][:] = scale * table[id_t][:], n rows of dim.
+ *   tokens   device, n ids, 32- or 64-bit signed integers (token_bits).
+ *   table    device, vocab x dim; out device, n x dim; bf16 or fp32 each.
+ * A negative id is padding: its row of out is zero. An id >= vocab also gives a zero row and is
+ * reported by muon_check_status (MUON_WARN_TOKEN). n may be 0.
+ */
+MUON_API int muon_embedding(const void* tokens, int token_bits, int64_t n, const void* table,
+                            muon_dtype_t table_dtype, int64_t table_stride, int64_t vocab, int64_t dim, float scale,
+                            void* out, muon_dtype_t out_dtype, int64_t out_stride, muon_stream_t stream);
+
+/*
+ * Its gradient by the table, from sorted tokens:
+ *   grad[v][:] = (accumulate ? grad[v][:] : 0) + scale * sum over t with id_t = v of dy[t][:]
+ * summed in fp32 in the order of t and rounded once. Without accumulate every row of grad is
+ * written (zeros for absent tokens); with it, the rows of absent tokens are not touched. Ids
+ * outside [0, vocab) contribute nothing (ids >= vocab are reported as above).
+ */
+MUON_API int64_t muon_embedding_grad_workspace(int64_t n, int64_t vocab, int64_t dim);
+MUON_API int muon_embedding_grad(const void* tokens, int token_bits, int64_t n, const void* dy, muon_dtype_t dy_dtype,
+                                 int64_t dy_stride, int64_t vocab, int64_t dim, float scale, void* grad,
+                                 muon_dtype_t grad_dtype, int64_t grad_stride, int accumulate, void* workspace,
+                                 int64_t workspace_bytes, muon_stream_t stream);
+
+/*
+ * Root-mean-square norm of rows x dim (dim <= 32768), with the residual's addition and an output
+ * in 8 bits with scales:
+ *   h = x + residual, rounded to the residual's type (h = x where residual is NULL; h is then
+ *       NULL too)
+ *   rstd[t] = 1 / sqrt(mean(h[t]^2) + eps)
+ *   y[t] = h[t] rstd[t] weight
+ *   codes, scales: the checkpoint of y before its rounding (see muon_checkpoint_store)
+ * y (x's type) or codes and scales may be NULL, not all of them. h may be the residual or x, and y
+ * may be x, where pointer, stride and type are the same.
+ */
+MUON_API int muon_rms_norm(const void* x, muon_dtype_t x_dtype, int64_t x_stride, const void* residual,
+                           muon_dtype_t r_dtype, int64_t r_stride, const void* weight, muon_dtype_t w_dtype,
+                           int64_t rows, int64_t dim, float eps, void* h, int64_t h_stride, void* y, int64_t y_stride,
+                           void* codes, int64_t codes_stride, void* scales, int64_t scales_stride, float* rstd,
+                           muon_stream_t stream);
+
+/*
+ * Its gradient, from the h and rstd of the forward pass; with n = h rstd and a = dy weight:
+ *   dx = rstd (a - n mean(a n)) + dh        (the gradient of h, and so of x and of the residual)
+ *   dweight = (accumulate ? dweight : 0) + sum over rows of dy n
+ * dh (NULL: none) and dx have h's type. dx may be dy, h or dh where pointer, stride and type are
+ * the same.
+ */
+MUON_API int64_t muon_rms_norm_grad_workspace(int64_t rows, int64_t dim);
+MUON_API int muon_rms_norm_grad(const void* dy, muon_dtype_t dy_dtype, int64_t dy_stride, const void* h,
+                                muon_dtype_t h_dtype, int64_t h_stride, const void* weight, muon_dtype_t w_dtype,
+                                const float* rstd, const void* dh, int64_t dh_stride, int64_t rows, int64_t dim, void* dx,
+                                int64_t dx_stride, float* dweight, int accumulate, void* workspace,
+                                int64_t workspace_bytes, muon_stream_t stream);
+
+/*
+ * 8-bit activation checkpoint of a matrix (the OCP microscaling format MXFP8 with e4m3 elements):
+ * every 32 consecutive elements of a row (fewer at its end) share a scale 2^e, held as one e8m0
+ * byte e + 127, with the smallest e of [-117, 119] for which no element exceeds 448 2^e; each
+ * element is rounded to the nearest e4m3 value of x 2^-e (ties to even; beyond 448 2^119 it
+ * saturates). Restored values are exact in bf16. A block with an infinity or a NaN gets the NaN
+ * scale (byte 255): all of it restores as NaN.
+ *   codes    device, rows x dim bytes; scales device, rows x ceil(dim / 32) bytes.
+ */
+MUON_API int muon_checkpoint_store(const void* x, muon_dtype_t x_dtype, int64_t x_stride, int64_t rows, int64_t dim,
+                                   void* codes, int64_t codes_stride, void* scales, int64_t scales_stride,
+                                   muon_stream_t stream);
+MUON_API int muon_checkpoint_restore(const void* codes, int64_t codes_stride, const void* scales,
+                                     int64_t scales_stride, int64_t rows, int64_t dim, void* x, muon_dtype_t x_dtype,
+                                     int64_t x_stride, muon_stream_t stream);
+
+/*
+ * Weight gradient of y = x W^T from dy and the checkpoint of x:
+ *   grad[i][j] = (accumulate ? grad[i][j] : 0) + sum over t of dy[t][i] x[t][j],  i < n, j < k
+ * on the tensor cores. An fp32 dy enters as three bf16 terms that sum to it exactly. rows <= 2^29,
+ * n and k <= 2^20; rows = 0 gives zeros (or leaves grad, accumulating). Waits inside the kernel are
+ * bounded as in muon_step (muon_set_wait_limit_ns, muon_check_status).
+ */
+MUON_API int64_t muon_weight_grad_workspace(int64_t rows, int64_t n, int64_t k, muon_dtype_t dy_dtype);
+MUON_API int muon_weight_grad(const void* dy, muon_dtype_t dy_dtype, int64_t dy_stride, const void* codes,
+                              int64_t codes_stride, const void* scales, int64_t scales_stride, int64_t rows, int64_t n,
+                              int64_t k, void* grad, muon_dtype_t grad_dtype, int64_t grad_stride, int accumulate,
+                              void* workspace, int64_t workspace_bytes, muon_stream_t stream);
+
 /* Message describing the last error returned on the calling thread ("" if none). The pointer
  * stays valid until the next call on that thread. */
 MUON_API const char* muon_last_error(void);
 
 /* Synchronises `stream`, then reads and clears the device status word of the current device.
  * Returns MUON_ERR_TIMEOUT if a kernel gave up waiting since the last check,
- * MUON_WARN_NONFINITE if a NaN or Inf reached an update matrix, MUON_OK otherwise
+ * MUON_WARN_TOKEN if an embedding call met a token id past the vocabulary, MUON_WARN_NONFINITE if
+ * a NaN or Inf reached an update matrix, MUON_OK otherwise (the first that applies; all are cleared)
  * (or MUON_ERR_CUDA if synchronising failed). */
 MUON_API int muon_check_status(muon_stream_t stream);
 
@@ -266,8 +369,8 @@ enum {
   MUON_KC_COUNT = 9
 };
 
-/* Turns per-launch timing on (nonzero) or off. While on, every kernel launch is bracketed by
- * CUDA events recorded on the launching stream. */
+/* Turns per-launch timing on (nonzero) or off. While on, every kernel launch of the classes above
+ * is bracketed by CUDA events recorded on the launching stream. */
 MUON_API int muon_profile_enable(int on);
 
 /* Synchronises the recorded events and returns, per kernel class, the number of launches and

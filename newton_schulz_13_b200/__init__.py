@@ -6,6 +6,9 @@ There is no CPU or PyTorch fallback; if the library is missing, importing this p
     import newton_schulz_13_b200 as ns
     ns.muon_step(params, grads, momentum, lr=0.02, mu=0.95)     # lists of CUDA tensors
     X = ns.ns_orthogonalize(G, steps=5)                          # one matrix
+
+The operators that make the gradients these steps take (ns.embedding, ns.rms_norm, ns.weight_grad
+and their companions) are in gradients.py.
 """
 from __future__ import annotations
 
@@ -19,7 +22,7 @@ LIB_PATH = os.path.join(HERE, "libmuon.so")
 BF16, FP32 = 0, 1
 PREC_BF16, PREC_FP32 = 0, 1
 RMS_ONE, RMS_SQRT_MAX1_ROWS_OVER_COLS = 0, 1
-OK, WARN_NONFINITE = 0, 1
+OK, WARN_NONFINITE, WARN_TOKEN = 0, 1, 2
 ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT = -1, -2, -3, -4, -5
 KC_CENTER, KC_PROLOGUE, KC_NORM, KC_GEMM, KC_EPILOGUE, KC_ADAMW = 0, 1, 2, 3, 4, 5
 KC_GEMM_GRAM, KC_GEMM_POLY, KC_GEMM_UPDATE, KC_COUNT = 6, 7, 8, 9
@@ -31,7 +34,10 @@ CUBIC = (1.5, -0.5, 0.0)
 
 EXPORTS = ["muon_ns_orthogonalize", "muon_step", "muon_adamw_step", "muon_last_error",
            "muon_check_status", "muon_release_workspace", "muon_profile_enable", "muon_profile_read",
-           "muon_launch_count", "muon_version", "muon_set_wave_elements", "muon_set_wait_limit_ns", "muon_set_chained_launch"]
+           "muon_launch_count", "muon_version", "muon_set_wave_elements", "muon_set_wait_limit_ns", "muon_set_chained_launch",
+           "muon_embedding", "muon_embedding_grad", "muon_embedding_grad_workspace", "muon_rms_norm",
+           "muon_rms_norm_grad", "muon_rms_norm_grad_workspace", "muon_checkpoint_store",
+           "muon_checkpoint_restore", "muon_weight_grad", "muon_weight_grad_workspace"]
 
 
 class MuonError(RuntimeError):
@@ -220,7 +226,7 @@ def adamw_step(params: List, grads: List, exp_avg: List, exp_avg_sq: List, step:
 
 
 def check_status(stream=None) -> int:
-    """Synchronises the stream and returns OK or WARN_NONFINITE; raises on a device timeout."""
+    """Synchronises the stream and returns OK, WARN_NONFINITE or WARN_TOKEN; raises on a device timeout."""
     return _check(lib.muon_check_status(_stream_handle(stream)))
 
 
@@ -268,3 +274,17 @@ def launch_count() -> int:
 
 def version() -> int:
     return int(lib.muon_version())
+
+
+# the operators that make the gradients; torch is imported with them, at their first use
+_GRADIENTS = ("ActCheckpoint", "RmsNorm", "MX_BLOCK", "embedding", "embedding_grad", "rms_norm", "rms_norm_grad",
+              "checkpoint_store", "checkpoint_restore", "weight_grad")
+
+
+def __getattr__(name: str):
+    if name in _GRADIENTS:
+        from . import gradients
+        for n in _GRADIENTS:
+            globals()[n] = getattr(gradients, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

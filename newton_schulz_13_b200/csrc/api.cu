@@ -1022,6 +1022,19 @@ void note_launches(int64_t n) {
   g_launches += n;
 }
 
+// Hook for the operators of ops_api.cu: the current device's SM count, status word and the wait
+// limit in force; fails (with the error message set) where there is no sm_100 device.
+int current_device_info(int* sms, int** status, uint64_t* wait_ns) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* ds = nullptr;
+  const int rc = device_state(&ds);
+  if (rc != MUON_OK) return rc;
+  if (sms) *sms = ds->sms;
+  if (status) *status = ds->d_status;
+  if (wait_ns) *wait_ns = g_wait_ns;
+  return MUON_OK;
+}
+
 }  // namespace muon
 
 using namespace muon;
@@ -1082,6 +1095,7 @@ int muon_check_status(muon_stream_t stream) {
   MUON_CUDA(cudaMemcpy(h, ds->d_status, sizeof(h), cudaMemcpyDeviceToHost));
   MUON_CUDA(cudaMemset(ds->d_status, 0, sizeof(h)));
   if (h[0] & kStatusTimeout) return fail(MUON_ERR_TIMEOUT, "a kernel wait hit its time limit");
+  if (h[0] & kStatusToken) return fail(MUON_WARN_TOKEN, "a token id was past the vocabulary");
   if (h[1] != 0) return fail(MUON_WARN_NONFINITE, std::to_string(h[1]) + " chunk(s) held NaN or Inf");
   return MUON_OK;
 }

@@ -19,6 +19,7 @@ constexpr int kCsCols = 256;
 
 // Device status word bits.
 constexpr int kStatusTimeout = 1;
+constexpr int kStatusToken = 2;   // a token id past the vocabulary (embedding, embedding gradient)
 
 // Per-matrix record read by the elementwise kernels.
 struct MatInfo {

@@ -1,0 +1,69 @@
+// Loads and stores of bf16 or fp32 values as fp32: eight at a time (16-byte accesses; the element
+// index and the base must make them aligned) or one at a time.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+namespace muon {
+
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* base, int64_t idx, float (&v)[8]) {
+  if constexpr (BF16) {
+    const uint4 raw = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + idx);
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&raw);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __bfloat1622float2(h[i]);
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  } else {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + idx);
+    const float4 a = p[0], b = p[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store8(void* base, int64_t idx, const float (&v)[8]) {
+  if constexpr (BF16) {
+    uint4 raw;
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&raw);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + idx) = raw;
+  } else {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + idx);
+    p[0] = make_float4(v[0], v[1], v[2], v[3]);
+    p[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ float load1(const void* base, int64_t idx) {
+  if constexpr (BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(base)[idx]);
+  else return static_cast<const float*>(base)[idx];
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store1(void* base, int64_t idx, float v) {
+  if constexpr (BF16) static_cast<__nv_bfloat16*>(base)[idx] = __float2bfloat16_rn(v);
+  else static_cast<float*>(base)[idx] = v;
+}
+
+// V = 8 or 1 elements, for kernels that serve aligned and unaligned rows with one body.
+template <int V, bool BF16>
+__device__ __forceinline__ void load_v(const void* base, int64_t idx, float (&v)[V]) {
+  if constexpr (V == 8) load8<BF16>(base, idx, v);
+  else v[0] = load1<BF16>(base, idx);
+}
+
+template <int V, bool BF16>
+__device__ __forceinline__ void store_v(void* base, int64_t idx, const float (&v)[V]) {
+  if constexpr (V == 8) store8<BF16>(base, idx, v);
+  else store1<BF16>(base, idx, v[0]);
+}
+
+}  // namespace muon
