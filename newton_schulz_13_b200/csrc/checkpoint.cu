@@ -15,19 +15,32 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Division of 31-bit numbers by a number of [1, 2^31) fixed per launch (a multiplication and a
+// shift): with s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1, n / d is
+// (umulhi(m, n) + n) >> s for every n < 2^31 (Granlund and Montgomery, "Division by invariant
+// integers using multiplication", 1994).
+struct Div {
+  uint32_t d, m, s;
+  explicit Div(uint32_t d_) : d(d_), m(0), s(0) {
+    while (s < 31 && (1u << s) < d) ++s;
+    m = (uint32_t)(((1ull << 32) * ((1ull << s) - d)) / d + 1);
+  }
+  __device__ __forceinline__ uint32_t quot(uint32_t n) const { return (__umulhi(m, n) + n) >> s; }
+};
+
+// per_row: 16-element pieces of a row, an even number; total: of all rows, below 2^31.
 template <bool X_BF16>
-__global__ void __launch_bounds__(kThreads) mx_store_kernel(MxArgs a) {
-  const int64_t per_row = (a.dim + 31) / 32 * 2;   // 16-element pieces, an even number
-  const int64_t total = a.rows * per_row;
-  // the loop bound is the same for both lanes of a block (total is even)
-  for (int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x; t < total; t += (int64_t)gridDim.x * kThreads) {
-    const int64_t row = t / per_row, p = t - row * per_row;
-    const int64_t c = p * 16;
+__global__ void __launch_bounds__(kThreads) mx_store_kernel(MxArgs a, Div per_row, uint32_t total) {
+  // the bound is the same for both lanes of a block (total is even)
+  const uint32_t t = blockIdx.x * kThreads + threadIdx.x;
+  if (t < total) {
+    const uint32_t row = per_row.quot(t), p = t - row * per_row.d;
+    const uint32_t c = p * 16;
     const bool ok = c < a.dim;   // dim is a multiple of 16
     float v[2][8] = {};
     if (ok) {
-      load8<X_BF16>(a.x, row * a.xs + c, v[0]);
-      load8<X_BF16>(a.x, row * a.xs + c + 8, v[1]);
+      load8<X_BF16>(a.x, (int64_t)row * a.xs + c, v[0]);
+      load8<X_BF16>(a.x, (int64_t)row * a.xs + c + 8, v[1]);
     }
     uint32_t m = 0;
 #pragma unroll
@@ -37,37 +50,37 @@ __global__ void __launch_bounds__(kThreads) mx_store_kernel(MxArgs a) {
     const uint32_t code = mx_scale_code(m);
     if (ok) {
       const uint2 lo = mx_pack8(v[0], code), hi = mx_pack8(v[1], code);
-      *reinterpret_cast<uint4*>(a.q + row * a.qs + c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-      if (!(p & 1)) a.sc[row * a.scs + p / 2] = (uint8_t)code;
+      *reinterpret_cast<uint4*>(a.q + (int64_t)row * a.qs + c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      if (!(p & 1)) a.sc[(int64_t)row * a.scs + p / 2] = (uint8_t)code;
     }
   }
 }
 
 template <bool X_BF16>
-__global__ void __launch_bounds__(kThreads) mx_store_any_kernel(MxArgs a) {
-  const int64_t per_row = (a.dim + 31) / 32, total = a.rows * per_row;
+__global__ void __launch_bounds__(kThreads) mx_store_any_kernel(MxArgs a, Div per_row, uint32_t total) {
   const int lane = threadIdx.x & 31;
-  for (int64_t b = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; b < total; b += ((int64_t)gridDim.x * kThreads) >> 5) {
-    const int64_t row = b / per_row, blk = b - row * per_row;
-    const int64_t c = blk * 32 + lane;
+  const uint32_t b = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);   // a 32-element block
+  if (b < total) {
+    const uint32_t row = per_row.quot(b), blk = b - row * per_row.d;
+    const uint32_t c = blk * 32 + lane;
     const bool ok = c < a.dim;
-    const float v = ok ? load1<X_BF16>(a.x, row * a.xs + c) : 0.0f;
+    const float v = ok ? load1<X_BF16>(a.x, (int64_t)row * a.xs + c) : 0.0f;
     uint32_t m = __float_as_uint(v) & 0x7fffffffu;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     const uint32_t code = mx_scale_code(m);
-    if (ok) a.q[row * a.qs + c] = (uint8_t)mx_pack1(v, code);
-    if (lane == 0) a.sc[row * a.scs + blk] = (uint8_t)code;
+    if (ok) a.q[(int64_t)row * a.qs + c] = (uint8_t)mx_pack1(v, code);
+    if (lane == 0) a.sc[(int64_t)row * a.scs + blk] = (uint8_t)code;
   }
 }
 
 template <bool O_BF16>
-__global__ void __launch_bounds__(kThreads) mx_restore_kernel(MxArgs a) {
-  const int64_t per_row = a.dim / 16, total = a.rows * per_row;
-  for (int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x; t < total; t += (int64_t)gridDim.x * kThreads) {
-    const int64_t row = t / per_row, p = t - row * per_row;
-    const uint4 raw = *reinterpret_cast<const uint4*>(a.q + row * a.qs + p * 16);
-    const float s = mx_scale(a.sc[row * a.scs + p / 2]);
+__global__ void __launch_bounds__(kThreads) mx_restore_kernel(MxArgs a, Div per_row, uint32_t total) {
+  const uint32_t t = blockIdx.x * kThreads + threadIdx.x;
+  if (t < total) {
+    const uint32_t row = per_row.quot(t), p = t - row * per_row.d;
+    const uint4 raw = *reinterpret_cast<const uint4*>(a.q + (int64_t)row * a.qs + p * 16);
+    const float s = mx_scale(a.sc[(int64_t)row * a.scs + p / 2]);
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     float v[2][8];
 #pragma unroll
@@ -76,18 +89,22 @@ __global__ void __launch_bounds__(kThreads) mx_restore_kernel(MxArgs a) {
       v[i >> 2][(2 * i) & 7] = f.x * s;
       v[i >> 2][(2 * i + 1) & 7] = f.y * s;
     }
-    store8<O_BF16>(a.out, row * a.xs + p * 16, v[0]);
-    store8<O_BF16>(a.out, row * a.xs + p * 16 + 8, v[1]);
+    store8<O_BF16>(a.out, (int64_t)row * a.xs + p * 16, v[0]);
+    store8<O_BF16>(a.out, (int64_t)row * a.xs + p * 16 + 8, v[1]);
   }
 }
 
 template <bool O_BF16>
-__global__ void __launch_bounds__(kThreads) mx_restore_any_kernel(MxArgs a) {
-  const int64_t total = a.rows * a.dim;
-  for (int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x; t < total; t += (int64_t)gridDim.x * kThreads) {
-    const int64_t row = t / a.dim, c = t - row * a.dim;
-    const float v = mx_unpack1(a.q[row * a.qs + c]) * mx_scale(a.sc[row * a.scs + c / 32]);
-    store1<O_BF16>(a.out, row * a.xs + c, v);
+__global__ void __launch_bounds__(kThreads) mx_restore_any_kernel(MxArgs a, Div per_row, uint32_t total) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t b = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);   // a 32-element block
+  if (b < total) {
+    const uint32_t row = per_row.quot(b), blk = b - row * per_row.d;
+    const uint32_t c = blk * 32 + lane;
+    if (c < a.dim) {
+      const float v = mx_unpack1(a.q[(int64_t)row * a.qs + c]) * mx_scale(a.sc[(int64_t)row * a.scs + blk]);
+      store1<O_BF16>(a.out, (int64_t)row * a.xs + c, v);
+    }
   }
 }
 
@@ -95,38 +112,51 @@ bool vec16(const MxArgs& a, const void* x) {
   return a.dim % 16 == 0 && (uintptr_t)x % 16 == 0 && a.xs % 8 == 0 && (uintptr_t)a.q % 16 == 0 && a.qs % 16 == 0;
 }
 
-int grid_of(int64_t threads, int sms) {
-  const int64_t b = (threads + kThreads - 1) / kThreads;
-  const int64_t cap = (int64_t)sms * 32;
-  return (int)(b < 1 ? 1 : (b < cap ? b : cap));
+// A row-contiguous matrix whose rows end on a block is one long row.
+MxArgs flat(MxArgs a) {
+  if (a.xs == a.dim && a.qs == a.dim && a.scs * 32 == a.dim && a.rows * a.dim < (int64_t(1) << 31)) {
+    a.dim *= a.rows;
+    a.xs = a.qs = a.dim;
+    a.scs = a.dim / 32;
+    a.rows = 1;
+  }
+  return a;
+}
+
+// Launches over all rows, `per_row` work items each and kThreads / `width` of them per block, in
+// runs of rows that keep the item index below 2^31.
+template <class K>
+cudaError_t launch_rows(MxArgs a, int64_t x_size, int64_t per_row, int width, K kernel, cudaStream_t s) {
+  const int64_t most = ((int64_t(1) << 31) - 1) / per_row;
+  for (int64_t r = 0; r < a.rows; r += most) {
+    MxArgs b = a;
+    b.rows = a.rows - r < most ? a.rows - r : most;
+    if (a.x) b.x = static_cast<const char*>(a.x) + r * a.xs * x_size;
+    if (a.out) b.out = static_cast<char*>(a.out) + r * a.xs * x_size;
+    b.q = a.q + r * a.qs;
+    b.sc = a.sc + r * a.scs;
+    const int64_t total = b.rows * per_row, per_block = kThreads / width;
+    kernel<<<(unsigned)((total + per_block - 1) / per_block), kThreads, 0, s>>>(b, Div((uint32_t)per_row), (uint32_t)total);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
 
-cudaError_t launch_mx_store(const MxArgs& a, int x_bf16, int sms, cudaStream_t s) {
-  if (vec16(a, a.x)) {
-    const int g = grid_of(a.rows * ((a.dim + 31) / 32 * 2), sms);
-    if (x_bf16) mx_store_kernel<true><<<g, kThreads, 0, s>>>(a);
-    else mx_store_kernel<false><<<g, kThreads, 0, s>>>(a);
-  } else {
-    const int g = grid_of(a.rows * ((a.dim + 31) / 32) * 32, sms);
-    if (x_bf16) mx_store_any_kernel<true><<<g, kThreads, 0, s>>>(a);
-    else mx_store_any_kernel<false><<<g, kThreads, 0, s>>>(a);
-  }
-  return cudaGetLastError();
+cudaError_t launch_mx_store(const MxArgs& args, int x_bf16, cudaStream_t s) {
+  const MxArgs a = flat(args);
+  const int64_t size = x_bf16 ? 2 : 4, blocks = (a.dim + 31) / 32;
+  if (vec16(a, a.x)) return launch_rows(a, size, blocks * 2, 1, x_bf16 ? mx_store_kernel<true> : mx_store_kernel<false>, s);
+  return launch_rows(a, size, blocks, 32, x_bf16 ? mx_store_any_kernel<true> : mx_store_any_kernel<false>, s);
 }
 
-cudaError_t launch_mx_restore(const MxArgs& a, int out_bf16, int sms, cudaStream_t s) {
-  if (vec16(a, a.out)) {
-    const int g = grid_of(a.rows * (a.dim / 16), sms);
-    if (out_bf16) mx_restore_kernel<true><<<g, kThreads, 0, s>>>(a);
-    else mx_restore_kernel<false><<<g, kThreads, 0, s>>>(a);
-  } else {
-    const int g = grid_of(a.rows * a.dim, sms);
-    if (out_bf16) mx_restore_any_kernel<true><<<g, kThreads, 0, s>>>(a);
-    else mx_restore_any_kernel<false><<<g, kThreads, 0, s>>>(a);
-  }
-  return cudaGetLastError();
+cudaError_t launch_mx_restore(const MxArgs& args, int out_bf16, cudaStream_t s) {
+  const MxArgs a = flat(args);
+  const int64_t size = out_bf16 ? 2 : 4, blocks = (a.dim + 31) / 32;
+  if (vec16(a, a.out)) return launch_rows(a, size, a.dim / 16, 1, out_bf16 ? mx_restore_kernel<true> : mx_restore_kernel<false>, s);
+  return launch_rows(a, size, blocks, 32, out_bf16 ? mx_restore_any_kernel<true> : mx_restore_any_kernel<false>, s);
 }
 
 }  // namespace muon

@@ -3,17 +3,20 @@
 // A negative id is padding: a zero row of out, nothing in grad. An id past the vocabulary is
 // treated the same way and recorded in the device status word.
 //
-// The gradient in three launches, with no atomics on data, so that its sums have one order:
-//   sort    each block owns a range of ids and reads all tokens: it counts the tokens below its
-//           range (where its part of the sorted list begins) and places its own, stably, by
-//           per-warp counts of each id. No block waits for another.
-//   sums    blocks of kRun sorted positions x a slice of columns add the rows of each run of
-//           equal ids in fp32; runs within a block go straight to grad, the parts of runs that
-//           cross its borders to a workspace. Further blocks zero the rows of ids that no token has.
-//   join    adds the parts of each crossing run in order.
+// The gradient in two launches, with no atomics on data, so that its sums have one order:
+//   sort    each block owns the ids of one residue modulo a power of two (frequent ids, which
+//           neighbour one another in most vocabularies, so fall to different blocks) and reads all
+//           tokens: it counts those of lower residues (where its part of the sorted list begins)
+//           and places its own, stably, by per-warp counts of each id. No block waits for another.
+//   sums    a warp adds the rows of one run of equal ids (of one piece of a long run) over 256
+//           columns in fp32, all its loads independent, and writes that part of the gradient;
+//           pieces go to a workspace, and the warp that finishes a run's last piece adds them in
+//           their order. Between these blocks lie others that zero the rows of absent ids: most
+//           of the bytes where the vocabulary is large.
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include "device_once.h"
 #include "muon_internal.h"
 #include "ops_internal.h"
 #include "ptx.cuh"
@@ -25,9 +28,13 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortIds = 1024;      // most ids of one block's range
-constexpr int kRun = 32;            // sorted positions per block of the sums
-constexpr int kFillRows = 16;       // ids per zero-filling block
+constexpr int kSortIds = 1024;      // most ids of one block
+constexpr int kBatch = 16;          // tokens per lane that a sort warp loads at a time
+constexpr int kWindow = 8;          // sorted places per block of the sums
+constexpr int kPiece = 16;          // rows per piece of a long run (the last piece: up to 31)
+constexpr int kLong = 32;           // runs from this length on are summed in pieces
+constexpr int kCols = 256;          // columns per warp
+constexpr int kFillRows = 32;       // ids per zero-filling block
 
 template <bool ID64>
 __device__ __forceinline__ int64_t load_id(const void* tokens, int64_t i) {
@@ -35,68 +42,103 @@ __device__ __forceinline__ int64_t load_id(const void* tokens, int64_t i) {
   else return static_cast<const int32_t*>(tokens)[i];
 }
 
+// A warp per row and part of kPart accesses per lane: the id is read once, the row's loads are
+// all in flight together.
+constexpr int kPart = 4;
+
 template <int V, bool T_BF16, bool O_BF16, bool ID64>
 __global__ void __launch_bounds__(kThreads) embedding_kernel(EmbedArgs a) {
-  const int64_t per_row = a.dim / V, total = a.n * per_row;
-  for (int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x; t < total; t += (int64_t)gridDim.x * kThreads) {
-    const int64_t row = t / per_row, c = (t - row * per_row) * V;
-    const int64_t id = load_id<ID64>(a.tokens, row);
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (row >= a.n) return;
+  const int64_t id = load_id<ID64>(a.tokens, row);
+  const int64_t c0 = ((int64_t)blockIdx.y * kPart * 32 + lane) * V;
+  const bool have = id >= 0 && id < a.vocab;
+  if (id >= a.vocab && c0 == 0) atomicOr(a.status, kStatusToken);
+  Raw<V, T_BF16> raw[kPart];
+#pragma unroll
+  for (int j = 0; j < kPart; ++j)
+    if (have && c0 + j * 32 * V < a.dim) raw[j].load(a.table, id * a.table_stride + c0 + j * 32 * V);
+#pragma unroll
+  for (int j = 0; j < kPart; ++j) {
+    const int64_t c = c0 + j * 32 * V;
+    if (c >= a.dim) break;
     float v[V];
-    if (id >= 0 && id < a.vocab) {
-      load_v<V, T_BF16>(a.table, id * a.table_stride + c, v);
+    if (have) {
+      raw[j].get(v);
 #pragma unroll
       for (int e = 0; e < V; ++e) v[e] *= a.scale;
     } else {
 #pragma unroll
       for (int e = 0; e < V; ++e) v[e] = 0.0f;
-      if (id >= a.vocab && c == 0) atomicOr(a.status, kStatusToken);
     }
     store_v<V, O_BF16>(a.out, row * a.out_stride + c, v);
   }
 }
 
-// ids: ids per block (at most kSortIds). Warps own consecutive segments of the tokens.
-template <bool ID64>
-__global__ void __launch_bounds__(kSortThreads, 1) token_sort_kernel(EmbedGradArgs a, int ids) {
-  extern __shared__ int cnt[];   // [kSortWarps][ids]
-  __shared__ int warp_part[kSortWarps];
+// Block b of gridDim.x = 1 << shift takes the ids v with v mod gridDim.x = b; ids: how many there
+// are at most. Warps own consecutive segments of the tokens and read them kBatch x 32 at a time; a
+// segment of one batch (up to 16,384 tokens in all) is read once. Cnt holds counts up to n.
+template <bool ID64, class Cnt>
+__global__ void __launch_bounds__(kSortThreads, 1) token_sort_kernel(EmbedGradArgs a, int ids, int shift, int slices) {
+  extern __shared__ int smem[];   // Cnt [kSortWarps][ids]: tokens of each id in each warp's segment
+  __shared__ int warp_part[kSortWarps], base[kSortIds], length[kSortIds];
+  Cnt* cnt = reinterpret_cast<Cnt*>(smem);
   grid_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t lo = (int64_t)blockIdx.x * ids;
-  const int here = (int)min((int64_t)ids, a.vocab - lo);
-  for (int i = threadIdx.x; i < kSortWarps * ids; i += kSortThreads) cnt[i] = 0;
-  __syncthreads();
+  const int me = blockIdx.x, mask = (1 << shift) - 1;
   const int64_t seg = (a.n + kSortThreads - 1) / kSortThreads * 32;
-  const int64_t t0 = warp * seg, t1 = min(a.n, t0 + seg);
-  int* mine = cnt + warp * ids;
+  const int64_t t0 = min(a.n, warp * seg), t1 = min(a.n, t0 + seg);
+  Cnt* mine = cnt + warp * ids;
   int below = 0;
   bool bad = false;
-  for (int64_t t = t0; t < t1; t += 32) {
-    const int64_t id = t + lane < t1 ? load_id<ID64>(a.tokens, t + lane) : -1;
-    below += id >= 0 && id < lo ? 1 : 0;
-    bad |= id >= a.vocab;
-    const bool in = id >= lo && id < lo + here;
-    if (!__any_sync(0xffffffffu, in)) continue;
-    const int b = in ? (int)(id - lo) : -1;
-    const uint32_t same = __match_any_sync(0xffffffffu, b);
-    if (in && lane == __ffs(same) - 1) mine[b] += __popc(same);
-    __syncwarp();
-  }
-  if (blockIdx.x == 0 && bad) atomicOr(a.status, kStatusToken);
+  int bin[kBatch];   // the id's number in this block, or -1
+  auto read = [&](int64_t t, bool count) {
+    int64_t id[kBatch];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) below += __shfl_xor_sync(0xffffffffu, below, o);
+    for (int j = 0; j < kBatch; ++j) id[j] = t + j * 32 + lane < t1 ? load_id<ID64>(a.tokens, t + j * 32 + lane) : -1;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const bool valid = id[j] >= 0 && id[j] < a.vocab;
+      const int r = (int)id[j] & mask;
+      if (count) {
+        below += valid && r < me ? 1 : 0;
+        bad |= id[j] >= a.vocab;
+      }
+      bin[j] = valid && r == me ? (int)(id[j] >> shift) : -1;
+    }
+  };
+  // lanes of one id among the lanes that have one (match only where there are several)
+  auto peers = [&](int k, uint32_t in) { return (in & (in - 1)) == 0 ? in : __match_any_sync(0xffffffffu, k); };
+  for (int i = threadIdx.x; i < (kSortWarps * ids * (int)sizeof(Cnt) + 3) / 4; i += kSortThreads) smem[i] = 0;
+  if (t0 < t1) read(t0, true);
+  __syncthreads();
+  for (int64_t t = t0; t < t1; t += kBatch * 32) {
+    if (t != t0) read(t, true);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const uint32_t in = __ballot_sync(0xffffffffu, bin[j] >= 0);
+      if (!in) continue;
+      const uint32_t same = peers(bin[j], in);
+      if (bin[j] >= 0 && lane == __ffs(same) - 1) mine[bin[j]] += (Cnt)__popc(same);
+      __syncwarp();
+    }
+  }
+  if (me == 0 && bad) atomicOr(a.status, kStatusToken);
+  below = __reduce_add_sync(0xffffffffu, below);
   if (lane == 0) warp_part[warp] = below;
   __syncthreads();
-  int first = 0;
-  for (int w = 0; w < kSortWarps; ++w) first += warp_part[w];
+  const int first = __reduce_add_sync(0xffffffffu, warp_part[lane]);
   __syncthreads();
   // one thread per id: counts before each warp, then a block scan over the ids
   const int b = threadIdx.x;
+  const int64_t id = ((int64_t)b << shift) + me;
   int total = 0;
-  if (b < here) {
+  if (b < ids) {
+#pragma unroll 8
     for (int w = 0; w < kSortWarps; ++w) {
       const int c = cnt[w * ids + b];
-      cnt[w * ids + b] = total;
+      cnt[w * ids + b] = (Cnt)total;
       total += c;
     }
   }
@@ -108,138 +150,214 @@ __global__ void __launch_bounds__(kSortThreads, 1) token_sort_kernel(EmbedGradAr
   }
   if (lane == 31) warp_part[warp] = scan;
   __syncthreads();
-  int before = first;
-  for (int w = 0; w < warp; ++w) before += warp_part[w];
-  const int begin = before + scan - total;
-  if (b < here) {
-    a.start[lo + b] = begin;
-    for (int w = 0; w < kSortWarps; ++w) cnt[w * ids + b] += begin;
-    if (lo + b == a.vocab - 1) a.start[a.vocab] = begin + total;
+  const int before = __reduce_add_sync(0xffffffffu, lane < warp ? warp_part[lane] : 0);
+  const int begin = first + before + scan - total;
+  if (b < ids) {
+    base[b] = begin;
+    length[b] = total;
+    if (id < a.vocab) a.total[id] = total;
+    if (total >= kLong)
+      for (int i = 0; i < slices; ++i) a.count[(int64_t)(begin / kPiece) * slices + i] = 0;
   }
+  if (me == mask && b == kSortThreads - 1) a.total[a.vocab] = begin + total;   // the last residue's end
   __syncthreads();
-  for (int64_t t = t0; t < t1; t += 32) {
-    const int64_t id = t + lane < t1 ? load_id<ID64>(a.tokens, t + lane) : -1;
-    const bool in = id >= lo && id < lo + here;
-    if (!__any_sync(0xffffffffu, in)) continue;
-    const int k = in ? (int)(id - lo) : -1;
-    const uint32_t same = __match_any_sync(0xffffffffu, k);
-    if (in) {
-      const int pos = mine[k] + __popc(same & ((1u << lane) - 1u));
-      a.order[pos] = (int)(t + lane);
-      a.keys[pos] = (int)id;
+  for (int64_t t = t0; t < t1; t += kBatch * 32) {
+    if (seg > kBatch * 32) read(t, false);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int k = bin[j];
+      const uint32_t in = __ballot_sync(0xffffffffu, k >= 0);
+      if (!in) continue;
+      const uint32_t same = peers(k, in);
+      if (k >= 0) {
+        const int place = mine[k] + __popc(same & ((1u << lane) - 1u));
+        a.sorted[base[k] + place] = make_int4((k << shift) + me, (int)(t + j * 32 + lane), place, length[k]);
+      }
+      __syncwarp();
+      if (k >= 0 && lane == __ffs(same) - 1) mine[k] += (Cnt)__popc(same);
+      __syncwarp();
     }
-    __syncwarp();
-    if (in && lane == __ffs(same) - 1) mine[k] += __popc(same);
-    __syncwarp();
   }
 }
+
+// fp32 values that other SMs have written during this kernel: read from L2, not from this SM's L1.
+template <int V>
+__device__ __forceinline__ void load_cg(const float* p, float (&v)[V]) {
+  if constexpr (V == 8) {
+    const float4 a = __ldcg(reinterpret_cast<const float4*>(p)), b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    v[0] = __ldcg(p);
+  }
+}
+
+// One lane's part of a warp's 256 columns: N accesses of V elements, 32 V apart.
+template <int V>
+struct Cols {
+  static constexpr int N = kCols / 32 / V;
+  int64_t c;       // first column
+  int64_t dim;
+  __device__ __forceinline__ bool ok(int j) const { return c + j * 32 * V < dim; }
+  __device__ __forceinline__ int64_t at(int j) const { return c + j * 32 * V; }
+};
 
 template <int V, bool G_BF16>
-__device__ __forceinline__ void write_grad(const EmbedGradArgs& a, int64_t id, int64_t c, float (&v)[V]) {
-  const int64_t at = id * a.grad_stride + c;
-  if (a.accumulate) {
-    float old[V];
-    load_v<V, G_BF16>(a.grad, at, old);
+__device__ __forceinline__ void write_grad(const EmbedGradArgs& a, int64_t id, const Cols<V>& w,
+                                           const Raw<V, G_BF16> (&old)[Cols<V>::N], float (&sum)[Cols<V>::N][V]) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = old[e] + a.scale * v[e];
-  } else {
+  for (int j = 0; j < Cols<V>::N; ++j) {
+    if (!w.ok(j)) continue;
+    float o[V], v[V];
+    if (a.accumulate) old[j].get(o);
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[e] *= a.scale;
+    for (int e = 0; e < V; ++e) v[e] = a.accumulate ? o[e] + a.scale * sum[j][e] : a.scale * sum[j][e];
+    store_v<V, G_BF16>(a.grad, id * a.grad_stride + w.at(j), v);
   }
-  store_v<V, G_BF16>(a.grad, at, v);
 }
 
-// Blocks [0, chunks): sums of one chunk of sorted positions over columns blockIdx.y * kThreads * V
-// onwards. Blocks [chunks, ...): zeros for ids without tokens (never launched when accumulating).
+// `sums` blocks for kWindow sorted places each, spread evenly among the blocks that write zeros
+// (none when accumulating): the sums wait on memory latency while the zeros fill its bandwidth.
 template <int V, bool D_BF16, bool G_BF16>
-__global__ void __launch_bounds__(kThreads) embed_sum_kernel(EmbedGradArgs a, int chunks) {
-  __shared__ int key[kRun + 2], ord[kRun];
+__global__ void __launch_bounds__(kThreads, V == 8 ? (D_BF16 ? 4 : 3) : 2) embed_sum_kernel(EmbedGradArgs a, int64_t sums, int64_t fills, int slices) {
+  constexpr int N = Cols<V>::N;
   grid_dependency_wait();
-  grid_launch_dependents();
-  const int64_t c = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * V;
-  if ((int64_t)blockIdx.x >= chunks) {
-    const int64_t v0 = ((int64_t)blockIdx.x - chunks) * kFillRows;
-    const int64_t v1 = min(a.vocab, v0 + kFillRows);
-    if (c >= a.dim) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t blk = blockIdx.x, all = sums + fills;
+  const int64_t before = blk * sums / all;     // sums blocks among the blocks before this one
+  if ((blk + 1) * sums / all == before) {
+    const int64_t v0 = (blk - before) * kFillRows + warp * (kFillRows / 8);
+    const bool mine = lane < kFillRows / 8 && v0 + lane < a.vocab;
+    const uint32_t absent = __ballot_sync(0xffffffffu, mine && a.total[mine ? v0 + lane : 0] == 0);
     float z[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) z[e] = 0.0f;
-    for (int64_t v = v0; v < v1; ++v)
-      if (a.start[v] == a.start[v + 1]) store_v<V, G_BF16>(a.grad, v * a.grad_stride + c, z);
+    for (int r = 0; r < kFillRows / 8; ++r) {
+      if (!(absent >> r & 1u)) continue;
+      const int64_t row = (v0 + r) * a.grad_stride;
+#pragma unroll 4
+      for (int64_t c = lane * V; c < a.dim; c += 32 * V) store_v<V, G_BF16>(a.grad, row + c, z);
+    }
     return;
   }
-  const int valid = a.start[a.vocab];
-  const int p0 = blockIdx.x * kRun;
+  // the places of the window and of the rows that its pieces may reach past it
+  const int64_t p0 = before * kWindow;
+  int4 me = make_int4(0, 0, 0, 0);
+  int far = 0;
+  if (p0 + lane < a.n) me = a.sorted[p0 + lane];
+  if (lane < kWindow && p0 + 32 + lane < a.n) far = a.sorted[p0 + 32 + lane].y;
+  const int64_t valid = a.total[a.vocab];
   if (p0 >= valid) return;
-  const int m = min(kRun, valid - p0);
-  for (int i = threadIdx.x; i < kRun + 2; i += blockDim.x) {   // key[i] belongs to position p0 + i - 1
-    const int p = p0 + i - 1;
-    key[i] = p >= 0 && p < valid ? a.keys[p] : -1;
-    if (i < m) ord[i] = a.order[p0 + i];
-  }
-  __syncthreads();
-  if (c >= a.dim) return;
-  float sum[V];
+  // the pieces that begin in this window: whole runs shorter than kLong, else every kPiece rows
+  // (the last piece takes the rest, so that pieces of long runs are at least kPiece apart)
+  const int pieces = me.w < kLong ? 1 : me.w / kPiece;
+  const bool head = lane < kWindow && p0 + lane < valid &&
+                    (me.w < kLong ? me.z == 0 : me.z % kPiece == 0 && me.z / kPiece < pieces);
+  const uint32_t heads = __ballot_sync(0xffffffffu, head);
+  const int rank = __popc(heads & ((1u << lane) - 1u));
+  const int items = __popc(heads) * slices;
+  for (int it = warp; it < items; it += kThreads / 32) {
+    const int slice = it % slices;
+    const int src = __ffs(__ballot_sync(0xffffffffu, head && rank == it / slices)) - 1;
+    const int id = __shfl_sync(0xffffffffu, me.x, src), off = __shfl_sync(0xffffffffu, me.z, src);
+    const int len = __shfl_sync(0xffffffffu, me.w, src), np = __shfl_sync(0xffffffffu, pieces, src);
+    const int64_t p = p0 + src;
+    const bool whole = np == 1;
+    const int n = whole ? len : (off / kPiece == np - 1 ? len - off : kPiece);   // at most 31 rows
+    const int near_pos = __shfl_sync(0xffffffffu, me.y, (src + lane) & 31);
+    const int far_pos = __shfl_sync(0xffffffffu, far, (src + lane) & 31);
+    const int pos = src + lane < 32 ? near_pos : far_pos;   // row of the piece's lane-th place
+    const Cols<V> w = {(int64_t)slice * kCols + lane * V, a.dim};
+    Raw<V, G_BF16> old[N];
+    if (a.accumulate && whole) {
 #pragma unroll
-  for (int e = 0; e < V; ++e) sum[e] = 0.0f;
-  bool from_before = key[0] == key[1];
-  constexpr int kAhead = 8;
-  for (int i0 = 0; i0 < m; i0 += kAhead) {
-    float v[kAhead][V];
+      for (int j = 0; j < N; ++j)
+        if (w.ok(j)) old[j].load(a.grad, id * a.grad_stride + w.at(j));
+    }
+    float sum[N][V];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (i0 + u < m) load_v<V, D_BF16>(a.dy, ord[i0 + u] * a.dy_stride + c, v[u]);
+    for (int j = 0; j < N; ++j)
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int i = i0 + u;
-      if (i >= m) break;
+      for (int e = 0; e < V; ++e) sum[j][e] = 0.0f;
+    constexpr int kAhead = 4;
+    for (int i0 = 0; i0 < n; i0 += kAhead) {
+      Raw<V, D_BF16> v[kAhead][N];
 #pragma unroll
-      for (int e = 0; e < V; ++e) sum[e] += v[u][e];
-      const bool ends = key[i + 2] != key[i + 1];
-      if (ends || i == m - 1) {
-        if (ends && !from_before) {
-          write_grad<V, G_BF16>(a, key[i + 1], c, sum);
-        } else {   // slot 0: a run that came from before; slot 1: one that begins here and goes on
-          store_v<V, false>(a.partial, ((int64_t)blockIdx.x * 2 + (from_before ? 0 : 1)) * a.dim + c, sum);
+      for (int u = 0; u < kAhead; ++u) {
+        if (i0 + u >= n) break;
+        const int64_t row = (int64_t)__shfl_sync(0xffffffffu, pos, i0 + u) * a.dy_stride;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (w.ok(j)) v[u][j].load(a.dy, row + w.at(j));
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (i0 + u >= n) break;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          if (!w.ok(j)) continue;
+          float f[V];
+          v[u][j].get(f);
+#pragma unroll
+          for (int e = 0; e < V; ++e) sum[j][e] += f[e];
         }
-#pragma unroll
-        for (int e = 0; e < V; ++e) sum[e] = 0.0f;
-        from_before = false;
       }
     }
-  }
-}
-
-// Block x joins the run that begins in chunk x and goes on past it.
-template <int V, bool G_BF16>
-__global__ void __launch_bounds__(kThreads) embed_join_kernel(EmbedGradArgs a) {
-  grid_dependency_wait();
-  const int valid = a.start[a.vocab];
-  const int64_t p1 = ((int64_t)blockIdx.x + 1) * kRun;
-  if (p1 >= valid) return;
-  const int id = a.keys[p1];
-  if (a.keys[p1 - 1] != id || a.start[id] < p1 - kRun) return;
-  const int64_t c = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * V;
-  if (c >= a.dim) return;
-  const int last = (a.start[id + 1] - 1) / kRun;
-  float sum[V];
-  load_v<V, false>(a.partial, ((int64_t)blockIdx.x * 2 + 1) * a.dim + c, sum);
-#pragma unroll 4
-  for (int k = (int)blockIdx.x + 1; k <= last; ++k) {
-    float v[V];
-    load_v<V, false>(a.partial, (int64_t)k * 2 * a.dim + c, v);
+    if (whole) {
+      write_grad<V, G_BF16>(a, id, w, old, sum);
+      continue;
+    }
+    // slot p / kPiece: no other piece of a long run has it. The run's slots follow one another.
+    const int64_t first = (p - off) / kPiece;
 #pragma unroll
-    for (int e = 0; e < V; ++e) sum[e] += v[e];
+    for (int j = 0; j < N; ++j)
+      if (w.ok(j)) store_v<V, false>(a.partial, (p / kPiece) * a.dim + w.at(j), sum[j]);
+    __threadfence();
+    __syncwarp();
+    int done = 0;
+    if (lane == 0) done = atomicAdd(a.count + first * slices + slice, 1);
+    if (__shfl_sync(0xffffffffu, done, 0) != np - 1) continue;
+    __threadfence();
+    if (a.accumulate) {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (w.ok(j)) old[j].load(a.grad, id * a.grad_stride + w.at(j));
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int e = 0; e < V; ++e) sum[j][e] = 0.0f;
+    constexpr int kParts = 2;
+    for (int k0 = 0; k0 < np; k0 += kParts) {
+      float v[kParts][N][V];
+#pragma unroll
+      for (int u = 0; u < kParts; ++u) {
+        if (k0 + u >= np) break;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (w.ok(j)) load_cg<V>(a.partial + (first + k0 + u) * a.dim + w.at(j), v[u][j]);
+      }
+#pragma unroll
+      for (int u = 0; u < kParts; ++u) {
+        if (k0 + u >= np) break;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          if (!w.ok(j)) continue;
+#pragma unroll
+          for (int e = 0; e < V; ++e) sum[j][e] += v[u][j][e];
+        }
+      }
+    }
+    write_grad<V, G_BF16>(a, id, w, old, sum);
   }
-  write_grad<V, G_BF16>(a, id, c, sum);
 }
 
 bool aligned8(const void* p, int64_t stride) { return (uintptr_t)p % 16 == 0 && stride % 8 == 0; }
 
 template <int V, bool T, bool O>
 cudaError_t embed_ids(const EmbedArgs& a, int id64, cudaStream_t s) {
-  const int64_t blocks = (a.n * (a.dim / V) + kThreads - 1) / kThreads;
-  const int grid = (int)(blocks < (1 << 20) ? blocks : (1 << 20));
+  const dim3 grid((unsigned)((a.n + kThreads / 32 - 1) / (kThreads / 32)),
+                  (unsigned)((a.dim + kPart * 32 * V - 1) / (kPart * 32 * V)));   // at most 8192 parts
   if (id64) embedding_kernel<V, T, O, true><<<grid, kThreads, 0, s>>>(a);
   else embedding_kernel<V, T, O, false><<<grid, kThreads, 0, s>>>(a);
   return cudaGetLastError();
@@ -253,21 +371,15 @@ cudaError_t embed_types(const EmbedArgs& a, int tb, int ob, int id64, cudaStream
   return embed_ids<V, false, false>(a, id64, s);
 }
 
+int slices_of(int64_t dim) { return (int)((dim + kCols - 1) / kCols); }
+
 template <int V, bool D, bool G>
 cudaError_t embed_sums(const EmbedGradArgs& a, int64_t* launches, cudaStream_t s) {
-  const int64_t per_row = a.dim / V;
-  int threads = 32;
-  while (threads < kThreads && threads < per_row) threads *= 2;
-  const unsigned slices = (unsigned)((per_row + threads - 1) / threads);
-  const int64_t chunks = (a.n + kRun - 1) / kRun;
-  const int64_t fill = a.accumulate ? 0 : (a.vocab + kFillRows - 1) / kFillRows;
-  cudaError_t e = launch_dependent(embed_sum_kernel<V, D, G>, dim3((unsigned)(chunks + fill), slices), dim3(threads), 0, s, a,
-                                   (int)chunks);
+  const int64_t sums = (a.n + kWindow - 1) / kWindow;
+  const int64_t fills = a.accumulate ? 0 : (a.vocab + kFillRows - 1) / kFillRows;
   ++*launches;
-  if (e != cudaSuccess || chunks < 2) return e;
-  e = launch_dependent(embed_join_kernel<V, G>, dim3((unsigned)(chunks - 1), slices), dim3(threads), 0, s, a);
-  ++*launches;
-  return e;
+  return launch_dependent(embed_sum_kernel<V, D, G>, dim3((unsigned)(sums + fills)), dim3(kThreads), 0, s, a, sums, fills,
+                          slices_of(a.dim));
 }
 
 template <int V>
@@ -288,29 +400,43 @@ cudaError_t launch_embedding(const EmbedArgs& a, int table_bf16, int out_bf16, i
 
 int64_t embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim, EmbedGradArgs* a, char* base) {
   auto up = [](int64_t b) { return (b + 255) / 256 * 256; };
-  const int64_t order = 0, keys = order + up(n * 4), start = keys + up(n * 4), partial = start + up((vocab + 1) * 4);
-  const int64_t chunks = (n + kRun - 1) / kRun;
+  const int64_t slots = (n + kPiece - 1) / kPiece;
+  const int64_t total = up(n * 16), partial = total + up((vocab + 1) * 4), count = partial + up(slots * dim * 4);
   if (a) {
-    a->order = reinterpret_cast<int*>(base + order);
-    a->keys = reinterpret_cast<int*>(base + keys);
-    a->start = reinterpret_cast<int*>(base + start);
+    a->sorted = reinterpret_cast<int4*>(base);
+    a->total = reinterpret_cast<int*>(base + total);
     a->partial = reinterpret_cast<float*>(base + partial);
+    a->count = reinterpret_cast<int*>(base + count);
   }
-  return partial + up(chunks * 2 * dim * 4);
+  return count + up(slots * slices_of(dim) * 4);
 }
 
-cudaError_t launch_embedding_grad(const EmbedGradArgs& a, int dy_bf16, int grad_bf16, int id64, int sms,
+cudaError_t launch_embedding_grad(const EmbedGradArgs& a, int dy_bf16, int grad_bf16, int id64,
                                   int64_t* launches, cudaStream_t s) {
-  // ranges of equal length, about one per SM
-  int64_t ids = (a.vocab + sms - 1) / sms;
-  if (ids > kSortIds) ids = kSortIds;
-  const int64_t blocks = (a.vocab + ids - 1) / ids;
-  const size_t smem = (size_t)kSortWarps * ids * sizeof(int);
-  const void* k = id64 ? (const void*)token_sort_kernel<true> : (const void*)token_sort_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortWarps * kSortIds * (int)sizeof(int));
+  // 128 residues (fewer for a small vocabulary, more where a residue would have over kSortIds ids)
+  int shift = 0;
+  while (shift < 7 && (a.vocab >> shift) > 64) ++shift;
+  while (((a.vocab - 1) >> shift) + 1 > kSortIds) ++shift;
+  const int ids = (int)(((a.vocab - 1) >> shift) + 1);
+  const bool small = a.n < 65536;   // counts fit 16 bits
+  const size_t smem = (size_t)kSortWarps * ids * (small ? 2 : 4) + 4;
+  using Kernel = void (*)(EmbedGradArgs, int, int, int);
+  const Kernel kernels[4] = {token_sort_kernel<false, int>, token_sort_kernel<false, uint16_t>,
+                             token_sort_kernel<true, int>, token_sort_kernel<true, uint16_t>};
+  static PerDeviceOnce once;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (id64) token_sort_kernel<true><<<(unsigned)blocks, kSortThreads, smem, s>>>(a, (int)ids);
-  else token_sort_kernel<false><<<(unsigned)blocks, kSortThreads, smem, s>>>(a, (int)ids);
+  e = (cudaError_t)once.run(dev, [&] {
+    for (const Kernel k : kernels) {
+      const cudaError_t r = cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 kSortWarps * kSortIds * 4 + 4);
+      if (r != cudaSuccess) return (int)r;
+    }
+    return 0;
+  });
+  if (e != cudaSuccess) return e;
+  kernels[(id64 ? 2 : 0) + (small ? 1 : 0)]<<<1u << shift, kSortThreads, smem, s>>>(a, ids, shift, slices_of(a.dim));
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   ++*launches;

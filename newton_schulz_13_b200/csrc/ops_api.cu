@@ -109,8 +109,7 @@ int muon_embedding(const void* tokens, int token_bits, int64_t n, const void* ta
             "out overlaps an input");
   if (n == 0) return MUON_OK;
   EmbedArgs a = {};
-  int sms = 0;
-  if (int rc = current_device_info(&sms, &a.status, nullptr)) return rc;
+  if (int rc = current_device_info(nullptr, &a.status, nullptr)) return rc;
   a.table = table;
   a.tokens = tokens;
   a.out = out;
@@ -154,8 +153,7 @@ int muon_embedding_grad(const void* tokens, int token_bits, int64_t n, const voi
             "grad or the workspace overlaps another buffer");
   if (n == 0 && accumulate) return MUON_OK;
   EmbedGradArgs a = {};
-  int sms = 0;
-  if (int rc = current_device_info(&sms, &a.status, nullptr)) return rc;
+  if (int rc = current_device_info(nullptr, &a.status, nullptr)) return rc;
   a.tokens = tokens;
   a.dy = dy;
   a.grad = grad;
@@ -168,7 +166,7 @@ int muon_embedding_grad(const void* tokens, int token_bits, int64_t n, const voi
   a.accumulate = accumulate != 0;
   embed_grad_workspace(n, vocab, dim, &a, static_cast<char*>(workspace));
   int64_t launches = 0;
-  const cudaError_t e = launch_embedding_grad(a, dy_dtype == MUON_BF16, grad_dtype == MUON_BF16, token_bits == 64, sms,
+  const cudaError_t e = launch_embedding_grad(a, dy_dtype == MUON_BF16, grad_dtype == MUON_BF16, token_bits == 64,
                                               &launches, reinterpret_cast<cudaStream_t>(stream));
   return finish(e, "embedding gradient launch", launches);
 }
@@ -328,11 +326,10 @@ int muon_checkpoint_store(const void* x, muon_dtype_t x_dtype, int64_t x_stride,
   set_error_message("");
   if (int rc = check_mx(x, x_dtype, x_stride, rows, dim, codes, codes_stride, scales, scales_stride, "x")) return rc;
   if (rows == 0) return MUON_OK;
-  int sms = 0;
-  if (int rc = current_device_info(&sms, nullptr, nullptr)) return rc;
+  if (int rc = current_device_info(nullptr, nullptr, nullptr)) return rc;
   MxArgs a = {x, nullptr, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales), rows, dim, x_stride, codes_stride,
               scales_stride};
-  return finish(launch_mx_store(a, x_dtype == MUON_BF16, sms, reinterpret_cast<cudaStream_t>(stream)),
+  return finish(launch_mx_store(a, x_dtype == MUON_BF16, reinterpret_cast<cudaStream_t>(stream)),
                 "checkpoint store launch", 1);
 }
 
@@ -342,11 +339,10 @@ int muon_checkpoint_restore(const void* codes, int64_t codes_stride, const void*
   set_error_message("");
   if (int rc = check_mx(x, x_dtype, x_stride, rows, dim, codes, codes_stride, scales, scales_stride, "x")) return rc;
   if (rows == 0) return MUON_OK;
-  int sms = 0;
-  if (int rc = current_device_info(&sms, nullptr, nullptr)) return rc;
+  if (int rc = current_device_info(nullptr, nullptr, nullptr)) return rc;
   MxArgs a = {nullptr, x, static_cast<uint8_t*>(const_cast<void*>(codes)),
               static_cast<uint8_t*>(const_cast<void*>(scales)), rows, dim, x_stride, codes_stride, scales_stride};
-  return finish(launch_mx_restore(a, x_dtype == MUON_BF16, sms, reinterpret_cast<cudaStream_t>(stream)),
+  return finish(launch_mx_restore(a, x_dtype == MUON_BF16, reinterpret_cast<cudaStream_t>(stream)),
                 "checkpoint restore launch", 1);
 }
 

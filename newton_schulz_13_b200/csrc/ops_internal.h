@@ -29,13 +29,13 @@ struct EmbedGradArgs {
   int accumulate;
   int* status;
   // workspace
-  int* order;      // [n] token positions sorted by id, in order of position within one id
-  int* keys;       // [n] their ids
-  int* start;      // [vocab + 1] first sorted position of each id; start[vocab] = number of valid tokens
-  float* partial;  // [chunks][2][dim] sums of the runs that cross a chunk's borders
+  int4* sorted;    // [n] tokens grouped by id: id, position, place in the run of the id, length of the run
+  int* total;      // [vocab + 1] tokens of each id; total[vocab] = tokens in all
+  float* partial;  // [ceil(n / 16)][dim] sums of the pieces of long runs
+  int* count;      // [ceil(n / 16)][slices] finished pieces of each long run
 };
 int64_t embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim, EmbedGradArgs* a, char* base);
-cudaError_t launch_embedding_grad(const EmbedGradArgs& a, int dy_bf16, int grad_bf16, int id64, int sms,
+cudaError_t launch_embedding_grad(const EmbedGradArgs& a, int dy_bf16, int grad_bf16, int id64,
                                   int64_t* launches, cudaStream_t s);
 
 // ---- RMS norm
@@ -79,8 +79,8 @@ struct MxArgs {
   uint8_t* sc;
   int64_t rows, dim, xs, qs, scs;
 };
-cudaError_t launch_mx_store(const MxArgs& a, int x_bf16, int sms, cudaStream_t s);
-cudaError_t launch_mx_restore(const MxArgs& a, int out_bf16, int sms, cudaStream_t s);
+cudaError_t launch_mx_store(const MxArgs& a, int x_bf16, cudaStream_t s);
+cudaError_t launch_mx_restore(const MxArgs& a, int out_bf16, cudaStream_t s);
 
 // ---- weight gradient
 struct WgradArgs {

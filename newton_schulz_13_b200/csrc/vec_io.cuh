@@ -53,6 +53,51 @@ __device__ __forceinline__ void store1(void* base, int64_t idx, float v) {
   else static_cast<float*>(base)[idx] = v;
 }
 
+// Eight values, or one, as loaded: kept so while several loads are in flight, and widened at use.
+template <int V, bool BF16>
+struct Raw;
+template <>
+struct Raw<8, true> {
+  uint4 r;
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    r = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __bfloat1622float2(h[i]);
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+};
+template <>
+struct Raw<8, false> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    a = q[0];
+    b = q[1];
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+template <>
+struct Raw<1, true> {
+  __nv_bfloat16 r;
+  __device__ __forceinline__ void load(const void* p, int64_t i) { r = static_cast<const __nv_bfloat16*>(p)[i]; }
+  __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = __bfloat162float(r); }
+};
+template <>
+struct Raw<1, false> {
+  float r;
+  __device__ __forceinline__ void load(const void* p, int64_t i) { r = static_cast<const float*>(p)[i]; }
+  __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = r; }
+};
+
 // V = 8 or 1 elements, for kernels that serve aligned and unaligned rows with one body.
 template <int V, bool BF16>
 __device__ __forceinline__ void load_v(const void* base, int64_t idx, float (&v)[V]) {

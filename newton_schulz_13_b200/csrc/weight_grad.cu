@@ -432,7 +432,7 @@ cudaError_t launch_wgrad(const WgradArgs& a, int dy_bf16, int grad_bf16, int sms
   m.xs = l.x_pitch;
   m.qs = a.qs;
   m.scs = a.scs;
-  cudaError_t e = launch_mx_restore(m, 1, sms, s);
+  cudaError_t e = launch_mx_restore(m, 1, s);
   if (e != cudaSuccess) return e;
   ++*launches;
   if (l.copy_dy) {
