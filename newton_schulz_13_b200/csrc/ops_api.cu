@@ -273,9 +273,9 @@ int muon_rms_norm_grad(const void* dy, muon_dtype_t dy_dtype, int64_t dy_stride,
   } else if (accumulate) {
     return MUON_OK;
   }
-  int sms = 0;
-  if (int rc = current_device_info(&sms, nullptr, nullptr)) return rc;
   NormGradArgs a = {};
+  int sms = 0;
+  if (int rc = current_device_info(&sms, &a.status, &a.wait_ns)) return rc;
   a.dy = dy;
   a.h = h;
   a.w = weight;

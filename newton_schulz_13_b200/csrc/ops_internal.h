@@ -66,6 +66,8 @@ struct NormGradArgs {
   int64_t rows, dim, dys, hs, dhs, dxs;
   int w_bf16, accumulate;
   float* partial;       // workspace: [blocks][dim]
+  int* status;
+  uint64_t wait_ns;
 };
 int64_t norm_grad_workspace(int64_t rows, int64_t dim);
 cudaError_t launch_rms_norm_grad(const NormGradArgs& a, int dy_bf16, int h_bf16, int sms, int64_t* launches,

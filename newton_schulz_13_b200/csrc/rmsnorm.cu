@@ -14,6 +14,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include "device_once.h"
+#include "muon_internal.h"
 #include "mx.cuh"
 #include "ops_internal.h"
 #include "ptx.cuh"
@@ -126,73 +128,211 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(NormArgs a) {
   }
 }
 
-// One row at a time per row group; each thread keeps the weight gradient of its own columns in
-// registers over all rows that its block takes (in a fixed order), and the blocks' sums are added
-// by norm_dw_kernel.
-template <int V, int VPT, bool DY_BF16, bool H_BF16>
-__global__ void __launch_bounds__(1024) rms_norm_grad_kernel(NormGradArgs a) {
-  extern __shared__ float dws[];   // [dim], only with several row groups
-  __shared__ float red[32 * 32];
+// How a row reaches the threads of the gradient:
+//   kBulk    one bulk copy per row and tensor into a ring of stages, S - 1 rows ahead (V = 8)
+//   kCopies  each thread copies its own accesses ahead, into slots that only it uses (V = 1, where
+//            rows begin on no 16-byte boundary)
+//   kDirect  no copies: a thread loads its accesses, twice (rows too long for the above)
+// 16384 x 4096 bf16 with dh, 537 MB: kBulk 82 us, per-thread copies 116-131 us, kDirect 125 us.
+enum class Feed { kBulk, kCopies, kDirect };
+
+// kCopies: where a thread's VPT accesses of each tensor lie in its slot. Slots are an odd number of
+// words apart, so that a warp's accesses to one place of its slots meet no bank twice.
+template <int VPT, bool DY_BF16, bool H_BF16>
+struct GradSlot {
+  static constexpr int kH = VPT * (DY_BF16 ? 2 : 4), kDh = kH + VPT * (H_BF16 ? 2 : 4);
+  static constexpr int odd(int bytes) { return ((bytes + 3) / 4 | 1) * 4; }
+  static constexpr int kPitch = odd(kDh), kPitchDh = odd(2 * kDh - kH);
+};
+
+// Copies one element into its slot: asynchronously if fp32.
+template <bool BF16>
+__device__ __forceinline__ void stage_element(char* slot, const void* base, int64_t i) {
+  if constexpr (BF16) *reinterpret_cast<__nv_bfloat16*>(slot) = static_cast<const __nv_bfloat16*>(base)[i];
+  else cp_async<4>(slot, static_cast<const float*>(base) + i);
+}
+
+constexpr int kGradGroups = 8, kGradStages = 4;
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+
+// A row group takes every (gridDim.x * groups)-th row; each thread keeps the weight gradient of its
+// own columns in registers over all of them (in a fixed order), and the blocks' sums are added by
+// norm_dw_kernel. A row costs one block barrier, its sum's.
+template <int V, int VPT, bool DY_BF16, bool H_BF16, Feed FEED, int S>
+__global__ void __launch_bounds__(FEED == Feed::kDirect ? 1024 : 512) rms_norm_grad_kernel(NormGradArgs a) {
+  extern __shared__ __align__(128) char slots[];   // the stages; after the rows, [dim] floats with several row groups
+  constexpr bool BULK = FEED == Feed::kBulk, COPIES = FEED == Feed::kCopies;
+  constexpr int kDy = DY_BF16 ? 2 : 4, kH = H_BF16 ? 2 : 4;
+  using L = GradSlot<VPT, DY_BF16, H_BF16>;
+  __shared__ float red[2][32];
+  __shared__ uint64_t full[kGradGroups][kGradStages];
+  __shared__ int abort_word[2];   // a wait gave up; never set (for the last waits)
   grid_launch_dependents();
-  const int tid = threadIdx.x, tpr = blockDim.x;
-  const int64_t nv = a.dim / V;
+  const int tid = threadIdx.x, tpr = blockDim.x, warps = tpr >> 5, group = threadIdx.y;
+  const int nv = (int)(a.dim / V), mine = tid < nv ? (nv - tid + tpr - 1) / tpr : 0;   // accesses of this thread
   const float inv_dim = 1.0f / (float)a.dim;
-  float dw[VPT][V];
+  const int64_t step = (int64_t)gridDim.x * blockDim.y, first = (int64_t)blockIdx.x * blockDim.y + group;
+  const bool leader = tid == 0;
+  bool timed_out = false;
+  int64_t fetched = 0;   // by this thread (kBulk)
+  if constexpr (BULK) {
+    if (leader) {
+      for (int s = 0; s < S; ++s) mbar_init(&full[group][s], 1);
+      if (group == 0) abort_word[0] = abort_word[1] = 0;
+      fence_mbar_init();
+    }
+    __syncthreads();
+  }
+  // bytes between stages, and this thread's (kCopies) or group's (kBulk) part of one
+  const int part = COPIES ? (a.dh ? L::kPitchDh : L::kPitch) : (int)a.dim * (kDy + (a.dh ? 2 : 1) * kH);
+  const int stage_bytes = part * (COPIES ? tpr * blockDim.y : blockDim.y);
+  char* const part0 = slots + part * (COPIES ? group * tpr + tid : group);
+  const int h_at = COPIES ? L::kH : (int)a.dim * kDy, dh_at = COPIES ? L::kDh : (int)a.dim * (kDy + kH);
+  // place of access j of a tensor of E-byte elements within its region of a part
+  auto at = [&](int j, int e) { return COPIES ? j * e : (j * tpr + tid) * V * e; };
+  auto fetch = [&](int64_t row, int s) {
+    char* const to = part0 + s * stage_bytes;
+    if constexpr (BULK) {
+      if (!leader || timed_out || row >= a.rows) return;
+      uint64_t* bar = &full[group][s];
+      mbar_arrive_expect_tx(bar, (uint32_t)part);
+      ++fetched;
+      bulk_load(to, static_cast<const char*>(a.dy) + row * a.dys * kDy, (uint32_t)a.dim * kDy, bar);
+      bulk_load(to + h_at, static_cast<const char*>(a.h) + row * a.hs * kH, (uint32_t)a.dim * kH, bar);
+      if (a.dh) bulk_load(to + dh_at, static_cast<const char*>(a.dh) + row * a.dhs * kH, (uint32_t)a.dim * kH, bar);
+    } else if constexpr (COPIES) {
+      if (row < a.rows) {
 #pragma unroll
-  for (int j = 0; j < VPT; ++j)
+        for (int j = 0; j < VPT; ++j) {
+          if (j >= mine) break;
+          const int64_t c = j * tpr + tid;
+          stage_element<DY_BF16>(to + at(j, kDy), a.dy, row * a.dys + c);
+          stage_element<H_BF16>(to + h_at + at(j, kH), a.h, row * a.hs + c);
+          if (a.dh) stage_element<H_BF16>(to + dh_at + at(j, kH), a.dh, row * a.dhs + c);
+        }
+      }
+      cp_async_commit();
+    }
+  };
+  float dw[VPT][V], w[VPT][V];
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) fetch(first + s * step, s);
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    if (FEED != Feed::kDirect && j < mine) load_w<V>(a.w, a.w_bf16, (int64_t)(j * tpr + tid) * V, w[j]);
 #pragma unroll
     for (int e = 0; e < V; ++e) dw[j][e] = 0.0f;
-  const int64_t step = (int64_t)gridDim.x * blockDim.y;
-  for (int64_t row0 = (int64_t)blockIdx.x * blockDim.y; row0 < a.rows; row0 += step) {
-    const int64_t row = row0 + threadIdx.y;
+  }
+  // rstd of this row and the rows ahead; with kCopies it is asked for with the copies of its row,
+  // since a load returns after the per-thread copies that were issued before it
+  constexpr int R = COPIES ? S - 1 : 1;
+  float rstds[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) rstds[k] = first + k * step < a.rows ? a.rstd[first + k * step] : 0.0f;
+  int s = 0, phase = 0, parity = 0;
+#pragma unroll 1
+  for (int64_t row = first; row - group < a.rows; row += step) {
     const bool on = row < a.rows;
-    float g[VPT][V], n[VPT][V];
-    float rstd = 0.0f;
+    const float rstd = rstds[0];
+#pragma unroll
+    for (int k = 0; k + 1 < R; ++k) rstds[k] = rstds[k + 1];
+    rstds[R - 1] = row + R * step < a.rows ? a.rstd[row + R * step] : 0.0f;
+    const char* const from = part0 + s * stage_bytes;
+    const int previous = s == 0 ? S - 1 : s - 1;
+    if constexpr (BULK) {
+      if (on && !mbar_wait_bounded(&full[group][s], phase, abort_word, a.wait_ns ? a.wait_ns : kTimeoutNs)) {
+        timed_out = true;
+        *(volatile int*)abort_word = 1;
+      }
+    } else if constexpr (COPIES) {
+      fetch(row + (S - 1) * step, previous);
+      cp_async_wait<S - 1>();
+    }
+    constexpr int KEEP = FEED == Feed::kDirect ? 1 : VPT;
+    float g[KEEP][V], n[KEEP][V];
+    // dy and h of access j (and its weights, where they are not kept)
+    auto read = [&](int j, float (&gj)[V], float (&nj)[V]) {
+      if constexpr (FEED != Feed::kDirect) {
+        load_v<V, DY_BF16>(from + at(j, kDy), 0, gj);
+        load_v<V, H_BF16>(from + h_at + at(j, kH), 0, nj);
+      } else {
+        const int64_t c = (int64_t)(j * tpr + tid) * V;
+        load_v<V, DY_BF16>(a.dy, row * a.dys + c, gj);
+        load_v<V, H_BF16>(a.h, row * a.hs + c, nj);
+        load_w<V>(a.w, a.w_bf16, c, w[0]);
+      }
+    };
+    float c = 0.0f;
     if (on) {
-      rstd = a.rstd[row];
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
-        const int64_t i = (int64_t)j * tpr + tid;
-        if (i < nv) {
-          load_v<V, DY_BF16>(a.dy, row * a.dys + i * V, g[j]);
-          load_v<V, H_BF16>(a.h, row * a.hs + i * V, n[j]);
-        }
-      }
-    }
-    float c = 0.0f;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int64_t i = (int64_t)j * tpr + tid;
-      if (on && i < nv) {
-        float w[V];
-        load_w<V>(a.w, a.w_bf16, i * V, w);
+        if (j >= mine) break;
+        float (&gj)[V] = g[KEEP > 1 ? j : 0], (&nj)[V] = n[KEEP > 1 ? j : 0], (&wj)[V] = w[KEEP > 1 ? j : 0];
+        read(j, gj, nj);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          n[j][e] *= rstd;
-          dw[j][e] += g[j][e] * n[j][e];
-          g[j][e] *= w[e];
-          c += g[j][e] * n[j][e];
+          nj[e] *= rstd;
+          dw[j][e] += gj[e] * nj[e];
+          gj[e] *= wj[e];
+          c += gj[e] * nj[e];
         }
       }
     }
-    c = row_sum(c, red) * inv_dim;
+    // the row's sum; the other half of red was last read before the barrier of the row before
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int64_t i = (int64_t)j * tpr + tid;
-      if (on && i < nv) {
+    for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    if (warps > 1) {
+      if ((tid & 31) == 0) red[parity][group * warps + (tid >> 5)] = c;
+      __syncthreads();
+      c = (tid & 31) < warps ? red[parity][group * warps + (tid & 31)] : 0.0f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+      parity ^= 1;
+    }
+    c *= inv_dim;
+    // past this barrier (of the warp, if it is the group) nobody reads the stage of the row before
+    if constexpr (BULK) fetch(row + (S - 1) * step, previous);
+    if (on) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        if (j >= mine) break;
+        float (&gj)[V] = g[KEEP > 1 ? j : 0], (&nj)[V] = n[KEEP > 1 ? j : 0];
+        if constexpr (FEED == Feed::kDirect) {
+          read(j, gj, nj);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            nj[e] *= rstd;
+            gj[e] *= w[0][e];
+          }
+        }
         float d[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) d[e] = rstd * (g[j][e] - n[j][e] * c);
+        for (int e = 0; e < V; ++e) d[e] = rstd * (gj[e] - nj[e] * c);
+        const int64_t col = (int64_t)(j * tpr + tid) * V;
         if (a.dh) {
           float r[V];
-          load_v<V, H_BF16>(a.dh, row * a.dhs + i * V, r);
+          if constexpr (FEED != Feed::kDirect) load_v<V, H_BF16>(from + dh_at + at(j, kH), 0, r);
+          else load_v<V, H_BF16>(a.dh, row * a.dhs + col, r);
 #pragma unroll
           for (int e = 0; e < V; ++e) d[e] += r[e];
         }
-        store_v<V, H_BF16>(a.dx, row * a.dxs + i * V, d);
+        store_v<V, H_BF16>(a.dx, row * a.dxs + col, d);
       }
     }
+    if (++s == S) {
+      s = 0;
+      phase ^= 1;
+    }
   }
+  if constexpr (BULK) {
+    if (timed_out) atomicOr(a.status, kStatusTimeout);
+    if (timed_out && leader) {
+      // no copy may land after the block has gone: wait for each stage's last one
+      for (int64_t f = fetched > S ? fetched - S : 0; f < fetched; ++f)
+        mbar_wait_bounded(&full[group][f % S], (f / S) & 1, abort_word + 1, kTimeoutNs);
+    }
+  }
+  float* dws = reinterpret_cast<float*>(slots);
   // the block's sum over its row groups, in their order
   if (blockDim.y > 1) {
     for (int gr = 0; gr < (int)blockDim.y; ++gr) {
@@ -222,18 +362,18 @@ __global__ void __launch_bounds__(1024) rms_norm_grad_kernel(NormGradArgs a) {
   }
 }
 
-// dw (+)= the sum of the blocks' partial sums: 32 columns per block, eight warps that take every
-// eighth partial in order, then the eight sums in order.
-__global__ void __launch_bounds__(256) norm_dw_kernel(const float* __restrict__ partial, float* dw, int blocks,
-                                                      int64_t dim, int accumulate) {
-  __shared__ float part[8][33];
+// dw (+)= the sum of the blocks' partial sums: 32 columns per block, 32 warps that take every 32nd
+// partial in order, then the 32 sums in order.
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__ partial, float* dw, int blocks,
+                                                       int64_t dim, int accumulate) {
+  __shared__ float part[32][33];
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t col = (int64_t)blockIdx.x * 32 + lane;
   float s = 0.0f;
   if (col < dim) {
 #pragma unroll 8
-    for (int b = w; b < blocks; b += 8) s += partial[(int64_t)b * dim + col];
+    for (int b = w; b < blocks; b += 32) s += partial[(int64_t)b * dim + col];
   }
   part[w][lane] = s;
   __syncthreads();
@@ -241,7 +381,7 @@ __global__ void __launch_bounds__(256) norm_dw_kernel(const float* __restrict__ 
     s = accumulate ? dw[col] : 0.0f;
     float t = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) t += part[k][lane];
+    for (int k = 0; k < 32; ++k) t += part[k][lane];
     dw[col] = s + t;
   }
 }
@@ -275,19 +415,47 @@ cudaError_t norm_types(const NormArgs& a, int xb, int rb, RowShape s, cudaStream
   return cudaGetLastError();
 }
 
-template <int V, int VPT, bool D, bool H>
-cudaError_t norm_grad_one(const NormGradArgs& a, RowShape s, int blocks, cudaStream_t st) {
-  const size_t smem = s.groups > 1 ? (size_t)a.dim * sizeof(float) : 0;   // at most 32 x VPT x V floats
-  rms_norm_grad_kernel<V, VPT, D, H><<<blocks, dim3(s.tpr, s.groups), smem, st>>>(a);
+constexpr int kGradSmem = 220 * 1024;   // of an SM, for the stages of its blocks
+
+template <int V, int VPT, bool D, bool H, Feed F, int S>
+cudaError_t norm_grad_one(const NormGradArgs& a, RowShape s, int64_t stage, int per_sm, int* blocks, cudaStream_t st) {
+  const int64_t sums = s.groups > 1 ? a.dim * (int64_t)sizeof(float) : 0, stages = S * stage;
+  const size_t smem = (size_t)(stages > sums ? stages : sums);
+  const int64_t groups = (a.rows + s.groups - 1) / s.groups, cap = (int64_t)kSms * per_sm;
+  *blocks = (int)(groups < cap ? groups : cap);
+  static PerDeviceOnce once;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = (cudaError_t)once.run(dev, [&] {
+    return (int)cudaFuncSetAttribute(rms_norm_grad_kernel<V, VPT, D, H, F, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kGradSmem);
+  });
+  if (e != cudaSuccess) return e;
+  rms_norm_grad_kernel<V, VPT, D, H, F, S><<<*blocks, dim3(s.tpr, s.groups), smem, st>>>(a);
   return cudaGetLastError();
 }
 
-template <int V, int VPT>
-cudaError_t norm_grad_types(const NormGradArgs& a, int db, int hb, RowShape s, int blocks, cudaStream_t st) {
-  if (db && hb) return norm_grad_one<V, VPT, true, true>(a, s, blocks, st);
-  if (db) return norm_grad_one<V, VPT, true, false>(a, s, blocks, st);
-  if (hb) return norm_grad_one<V, VPT, false, true>(a, s, blocks, st);
-  return norm_grad_one<V, VPT, false, false>(a, s, blocks, st);
+// Blocks of 256 threads, two per SM, or one of 512; rows ahead as their stages leave room for.
+template <int V, int VPT, bool D, bool H, Feed F>
+cudaError_t norm_grad_stages(const NormGradArgs& a, int* blocks, cudaStream_t st) {
+  const RowShape s = row_shape(a.dim / V, VPT, 256);
+  const int per_sm = s.tpr <= 256 ? 2 : 1;
+  const int64_t stage = F == Feed::kBulk
+                            ? s.groups * a.dim * ((D ? 2 : 4) + (a.dh ? 2 : 1) * (H ? 2 : 4))
+                            : s.groups * s.tpr * (a.dh ? GradSlot<VPT, D, H>::kPitchDh : GradSlot<VPT, D, H>::kPitch);
+  if (stage * kGradStages * per_sm <= kGradSmem)
+    return norm_grad_one<V, VPT, D, H, F, kGradStages>(a, s, stage, per_sm, blocks, st);
+  return norm_grad_one<V, VPT, D, H, F, 2>(a, s, stage, per_sm, blocks, st);
+}
+
+template <bool D, bool H>
+cudaError_t norm_grad_shapes(const NormGradArgs& a, bool v8, int* blocks, cudaStream_t st) {
+  if (v8 && a.dim <= 8192) return norm_grad_stages<8, 2, D, H, Feed::kBulk>(a, blocks, st);
+  if (v8) return norm_grad_one<8, 4, D, H, Feed::kDirect, 1>(a, row_shape(a.dim / 8, 4, 256), 0, 1, blocks, st);
+  if (a.dim <= 4096) return norm_grad_stages<1, 8, D, H, Feed::kCopies>(a, blocks, st);
+  if (a.dim <= 8192) return norm_grad_stages<1, 16, D, H, Feed::kCopies>(a, blocks, st);
+  return norm_grad_one<1, 32, D, H, Feed::kDirect, 1>(a, row_shape(a.dim, 32, 256), 0, 1, blocks, st);
 }
 
 int norm_grad_blocks(int64_t rows) {
@@ -321,27 +489,19 @@ int64_t norm_grad_workspace(int64_t rows, int64_t dim) {
 cudaError_t launch_rms_norm_grad(const NormGradArgs& a, int dy_bf16, int h_bf16, int sms, int64_t* launches,
                                  cudaStream_t st) {
   if (a.rows == 0) {   // the empty sum
-    norm_dw_kernel<<<(unsigned)((a.dim + 31) / 32), 256, 0, st>>>(a.partial, a.dw, 0, a.dim, a.accumulate);
+    norm_dw_kernel<<<(unsigned)((a.dim + 31) / 32), 1024, 0, st>>>(a.partial, a.dw, 0, a.dim, a.accumulate);
     ++*launches;
     return cudaGetLastError();
   }
   const bool v8 = a.dim % 8 == 0 && (uintptr_t)a.w % 16 == 0 && aligned8(a.dy, a.dys, dy_bf16) &&
                   aligned8(a.h, a.hs, h_bf16) && aligned8(a.dx, a.dxs, h_bf16) &&
                   (!a.dh || aligned8(a.dh, a.dhs, h_bf16));
-  const RowShape s = v8 ? row_shape(a.dim / 8, 2, 128) : row_shape(a.dim, 8, 128);
-  int blocks = norm_grad_blocks((a.rows + s.groups - 1) / s.groups);
-  cudaError_t e;
-  if (v8) {
-    e = s.vpt <= 1   ? norm_grad_types<8, 1>(a, dy_bf16, h_bf16, s, blocks, st)
-        : s.vpt <= 2 ? norm_grad_types<8, 2>(a, dy_bf16, h_bf16, s, blocks, st)
-                     : norm_grad_types<8, 4>(a, dy_bf16, h_bf16, s, blocks, st);
-  } else {
-    e = s.vpt <= 8 ? norm_grad_types<1, 8>(a, dy_bf16, h_bf16, s, blocks, st)
-                   : norm_grad_types<1, 32>(a, dy_bf16, h_bf16, s, blocks, st);
-  }
+  int blocks = 0;   // at most norm_grad_blocks(rows)
+  cudaError_t e = dy_bf16 ? (h_bf16 ? norm_grad_shapes<true, true>(a, v8, &blocks, st) : norm_grad_shapes<true, false>(a, v8, &blocks, st))
+                          : (h_bf16 ? norm_grad_shapes<false, true>(a, v8, &blocks, st) : norm_grad_shapes<false, false>(a, v8, &blocks, st));
   if (e != cudaSuccess) return e;
   ++*launches;
-  e = launch_dependent(norm_dw_kernel, dim3((unsigned)((a.dim + 31) / 32)), dim3(256), 0, st,
+  e = launch_dependent(norm_dw_kernel, dim3((unsigned)((a.dim + 31) / 32)), dim3(1024), 0, st,
                        (const float*)a.partial, a.dw, blocks, a.dim, a.accumulate);
   ++*launches;
   return e;
