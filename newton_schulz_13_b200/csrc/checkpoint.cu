@@ -1,8 +1,8 @@
 // 8-bit activation checkpoints (mx.cuh): store (quantise) and restore.
 //
 // Bound by HBM: 2 or 4 bytes read and 1 + 1/32 written per element on the way in, the reverse on
-// the way out. Aligned rows: a thread owns 16 consecutive elements, two lanes a 32-element block;
-// other rows: a lane owns one element, a warp one block.
+// the way out. Aligned rows: a thread owns eight consecutive elements of two places, four lanes a
+// 32-element block; other rows: a lane owns one element, a warp one block.
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -28,30 +28,35 @@ struct Div {
   __device__ __forceinline__ uint32_t quot(uint32_t n) const { return (__umulhi(m, n) + n) >> s; }
 };
 
-// per_row: 16-element pieces of a row, an even number; total: of all rows, below 2^31.
+constexpr int kAcc = 2;   // accesses per thread, kThreads apart
+
+// per_row: 8-element accesses of a row, padded to whole blocks (a multiple of 4); total: of all
+// rows, below 2^31.
 template <bool X_BF16>
 __global__ void __launch_bounds__(kThreads) mx_store_kernel(MxArgs a, Div per_row, uint32_t total) {
-  // the bound is the same for both lanes of a block (total is even)
-  const uint32_t t = blockIdx.x * kThreads + threadIdx.x;
-  if (t < total) {
-    const uint32_t row = per_row.quot(t), p = t - row * per_row.d;
-    const uint32_t c = p * 16;
-    const bool ok = c < a.dim;   // dim is a multiple of 16
-    float v[2][8] = {};
-    if (ok) {
-      load8<X_BF16>(a.x, (int64_t)row * a.xs + c, v[0]);
-      load8<X_BF16>(a.x, (int64_t)row * a.xs + c + 8, v[1]);
-    }
-    uint32_t m = 0;
+  const uint32_t t0 = blockIdx.x * (kAcc * kThreads) + threadIdx.x;
+  Raw<8, X_BF16> raw[kAcc];
+  uint32_t row[kAcc], c[kAcc];
+  bool ok[kAcc];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = max(m, max(__float_as_uint(v[0][e]) & 0x7fffffffu, __float_as_uint(v[1][e]) & 0x7fffffffu));
-    const uint32_t pair = 3u << (threadIdx.x & 30);
-    m = max(m, __shfl_xor_sync(pair, m, 1));
+  for (int j = 0; j < kAcc; ++j) {
+    const uint32_t t = t0 + j * kThreads;
+    row[j] = per_row.quot(t);
+    c[j] = (t - row[j] * per_row.d) * 8;
+    ok[j] = t < total && c[j] < a.dim;   // dim is a multiple of 8
+    if (ok[j]) raw[j].load(a.x, (int64_t)row[j] * a.xs + c[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < kAcc; ++j) {
+    float v[8] = {};
+    if (ok[j]) raw[j].get(v);
+    uint32_t m = mx_amax8(v);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));   // the four lanes of a block
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const uint32_t code = mx_scale_code(m);
-    if (ok) {
-      const uint2 lo = mx_pack8(v[0], code), hi = mx_pack8(v[1], code);
-      *reinterpret_cast<uint4*>(a.q + (int64_t)row * a.qs + c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-      if (!(p & 1)) a.sc[(int64_t)row * a.scs + p / 2] = (uint8_t)code;
+    if (ok[j]) {
+      *reinterpret_cast<uint2*>(a.q + (int64_t)row[j] * a.qs + c[j]) = mx_pack8(v, code);
+      if (!(c[j] & (kMxBlock - 1))) a.sc[(int64_t)row[j] * a.scs + c[j] / kMxBlock] = (uint8_t)code;
     }
   }
 }
@@ -76,21 +81,30 @@ __global__ void __launch_bounds__(kThreads) mx_store_any_kernel(MxArgs a, Div pe
 
 template <bool O_BF16>
 __global__ void __launch_bounds__(kThreads) mx_restore_kernel(MxArgs a, Div per_row, uint32_t total) {
-  const uint32_t t = blockIdx.x * kThreads + threadIdx.x;
-  if (t < total) {
-    const uint32_t row = per_row.quot(t), p = t - row * per_row.d;
-    const uint4 raw = *reinterpret_cast<const uint4*>(a.q + (int64_t)row * a.qs + p * 16);
-    const float s = mx_scale(a.sc[(int64_t)row * a.scs + p / 2]);
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    float v[2][8];
+  const uint32_t t0 = blockIdx.x * (kAcc * kThreads) + threadIdx.x;
+  uint2 raw[kAcc];
+  uint32_t row[kAcc], c[kAcc], code[kAcc];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 f = mx_unpack2(w[i >> 1] >> (16 * (i & 1)));
-      v[i >> 2][(2 * i) & 7] = f.x * s;
-      v[i >> 2][(2 * i + 1) & 7] = f.y * s;
+  for (int j = 0; j < kAcc; ++j) {
+    const uint32_t t = t0 + j * kThreads;
+    row[j] = per_row.quot(t);
+    c[j] = (t - row[j] * per_row.d) * 8;
+    if (t >= total) continue;
+    raw[j] = *reinterpret_cast<const uint2*>(a.q + (int64_t)row[j] * a.qs + c[j]);
+    code[j] = a.sc[(int64_t)row[j] * a.scs + c[j] / kMxBlock];
+  }
+#pragma unroll
+  for (int j = 0; j < kAcc; ++j) {
+    if (t0 + j * kThreads >= total) break;
+    const float s = mx_scale(code[j]);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __fmul2_rn(mx_unpack2((i < 2 ? raw[j].x : raw[j].y) >> (16 * (i & 1))), make_float2(s, s));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
     }
-    store8<O_BF16>(a.out, (int64_t)row * a.xs + p * 16, v[0]);
-    store8<O_BF16>(a.out, (int64_t)row * a.xs + p * 16 + 8, v[1]);
+    store8<O_BF16>(a.out, (int64_t)row[j] * a.xs + c[j], v);
   }
 }
 
@@ -108,8 +122,8 @@ __global__ void __launch_bounds__(kThreads) mx_restore_any_kernel(MxArgs a, Div 
   }
 }
 
-bool vec16(const MxArgs& a, const void* x) {
-  return a.dim % 16 == 0 && (uintptr_t)x % 16 == 0 && a.xs % 8 == 0 && (uintptr_t)a.q % 16 == 0 && a.qs % 16 == 0;
+bool vec8(const MxArgs& a, const void* x) {
+  return a.dim % 8 == 0 && (uintptr_t)x % 16 == 0 && a.xs % 8 == 0 && (uintptr_t)a.q % 8 == 0 && a.qs % 8 == 0;
 }
 
 // A row-contiguous matrix whose rows end on a block is one long row.
@@ -123,10 +137,10 @@ MxArgs flat(MxArgs a) {
   return a;
 }
 
-// Launches over all rows, `per_row` work items each and kThreads / `width` of them per block, in
+// Launches over all rows, `per_row` work items each and `per_block` of them per block, in
 // runs of rows that keep the item index below 2^31.
 template <class K>
-cudaError_t launch_rows(MxArgs a, int64_t x_size, int64_t per_row, int width, K kernel, cudaStream_t s) {
+cudaError_t launch_rows(MxArgs a, int64_t x_size, int64_t per_row, int64_t per_block, K kernel, cudaStream_t s) {
   const int64_t most = ((int64_t(1) << 31) - 1) / per_row;
   for (int64_t r = 0; r < a.rows; r += most) {
     MxArgs b = a;
@@ -135,7 +149,7 @@ cudaError_t launch_rows(MxArgs a, int64_t x_size, int64_t per_row, int width, K 
     if (a.out) b.out = static_cast<char*>(a.out) + r * a.xs * x_size;
     b.q = a.q + r * a.qs;
     b.sc = a.sc + r * a.scs;
-    const int64_t total = b.rows * per_row, per_block = kThreads / width;
+    const int64_t total = b.rows * per_row;
     kernel<<<(unsigned)((total + per_block - 1) / per_block), kThreads, 0, s>>>(b, Div((uint32_t)per_row), (uint32_t)total);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -148,15 +162,15 @@ cudaError_t launch_rows(MxArgs a, int64_t x_size, int64_t per_row, int width, K 
 cudaError_t launch_mx_store(const MxArgs& args, int x_bf16, cudaStream_t s) {
   const MxArgs a = flat(args);
   const int64_t size = x_bf16 ? 2 : 4, blocks = (a.dim + 31) / 32;
-  if (vec16(a, a.x)) return launch_rows(a, size, blocks * 2, 1, x_bf16 ? mx_store_kernel<true> : mx_store_kernel<false>, s);
-  return launch_rows(a, size, blocks, 32, x_bf16 ? mx_store_any_kernel<true> : mx_store_any_kernel<false>, s);
+  if (vec8(a, a.x)) return launch_rows(a, size, blocks * 4, kAcc * kThreads, x_bf16 ? mx_store_kernel<true> : mx_store_kernel<false>, s);
+  return launch_rows(a, size, blocks, kThreads / 32, x_bf16 ? mx_store_any_kernel<true> : mx_store_any_kernel<false>, s);
 }
 
 cudaError_t launch_mx_restore(const MxArgs& args, int out_bf16, cudaStream_t s) {
   const MxArgs a = flat(args);
   const int64_t size = out_bf16 ? 2 : 4, blocks = (a.dim + 31) / 32;
-  if (vec16(a, a.out)) return launch_rows(a, size, a.dim / 16, 1, out_bf16 ? mx_restore_kernel<true> : mx_restore_kernel<false>, s);
-  return launch_rows(a, size, blocks, 32, out_bf16 ? mx_restore_any_kernel<true> : mx_restore_any_kernel<false>, s);
+  if (vec8(a, a.out)) return launch_rows(a, size, a.dim / 8, kAcc * kThreads, out_bf16 ? mx_restore_kernel<true> : mx_restore_kernel<false>, s);
+  return launch_rows(a, size, blocks, kThreads / 32, out_bf16 ? mx_restore_any_kernel<true> : mx_restore_any_kernel<false>, s);
 }
 
 }  // namespace muon

@@ -22,10 +22,20 @@ constexpr uint32_t kMxNan = 255;
 // maximum of |x| bits orders finite values, then infinity, then NaN).
 __device__ __forceinline__ uint32_t mx_scale_code(uint32_t amax_bits) {
   if (amax_bits >= 0x7f800000u) return kMxNan;
-  // 448 = 1.75 2^8: x = f 2^E with f in [1, 2) needs e = E - 8, or one more when f > 1.75
-  int e = (int)(amax_bits >> 23) - 127 - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-  e = max(kMxExpMin, min(kMxExpMax, e));
-  return (uint32_t)(e + 127);
+  // 448 = 1.75 2^8: x = f 2^E with f in [1, 2) needs e = E - 8, or one more when f > 1.75 (then the
+  // sum carries into the exponent)
+  const int code = (int)((amax_bits + 0x1fffffu) >> 23) - 8;
+  return (uint32_t)max(kMxExpMin + 127, min(kMxExpMax + 127, code));
+}
+
+// Bits of max |v| of eight values; NaN if one of them is.
+__device__ __forceinline__ uint32_t mx_amax8(const float (&v)[8]) {
+  float m = fabsf(v[0]);
+  asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(fabsf(v[1])), "f"(fabsf(v[2])));
+  asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(fabsf(v[3])), "f"(fabsf(v[4])));
+  asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(fabsf(v[5])), "f"(fabsf(v[6])));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v[7])));
+  return __float_as_uint(m) & 0x7fffffffu;
 }
 
 // 2^-e as a float for a scale code that mx_scale_code returned (not for the NaN code).
@@ -52,9 +62,14 @@ __device__ __forceinline__ uint32_t mx_pack1(float v, uint32_t code) {
 
 __device__ __forceinline__ uint2 mx_pack8(const float (&v)[8], uint32_t code) {
   if (code == kMxNan) return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-  const float s = mx_inv_scale(code);
-  return make_uint2(mx_pack2(v[0] * s, v[1] * s) | (mx_pack2(v[2] * s, v[3] * s) << 16),
-                    mx_pack2(v[4] * s, v[5] * s) | (mx_pack2(v[6] * s, v[7] * s) << 16));
+  const float2 s = make_float2(mx_inv_scale(code), mx_inv_scale(code));
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), s);
+    c[i] = mx_pack2(p.x, p.y);
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
 // Values of the two e4m3 codes in the low 16 bits.

@@ -206,9 +206,9 @@ int muon_rms_norm(const void* x, muon_dtype_t x_dtype, int64_t x_stride, const v
             "scales overlap another buffer");
   REFUSE_IF(share(T, X) || share(T, R) || share(T, W) || share(T, H) || share(T, Y) || share(T, Q) || share(T, S),
             "rstd overlaps another buffer");
-  int sms = 0;
-  if (int rc = current_device_info(&sms, nullptr, nullptr)) return rc;
   NormArgs a = {};
+  int sms = 0;
+  if (int rc = current_device_info(&sms, &a.status, &a.wait_ns)) return rc;
   a.x = x;
   a.r = residual;
   a.w = weight;

@@ -52,6 +52,8 @@ struct NormArgs {
   int64_t rows, dim, xs, rs, hs, ys, qs, scs;
   float eps;
   int w_bf16;
+  int* status;
+  uint64_t wait_ns;
 };
 cudaError_t launch_rms_norm(const NormArgs& a, int x_bf16, int r_bf16, int sms, cudaStream_t s);
 

@@ -6,11 +6,12 @@
 // All sums and statistics are fp32. The norm is taken of the rounded h, which is what the gradient
 // reads back, and the checkpoint of the unrounded y, so each of its values is rounded once.
 //
-// Both are bound by HBM: every element is read and written once. A row belongs to `tpr` threads
-// (a multiple of 32) that hold it in registers, VPT accesses of V elements each: V = 8 (16-byte
-// accesses) when every row is aligned to eight elements, V = 1 otherwise, where a warp reads 32
-// consecutive elements per access. In both, a 32-element checkpoint block lies within a warp: four
-// lanes of one access (V = 8) or all 32 (V = 1).
+// Both are bound by HBM: every element is read and written once (16384 x 4096 bf16 with residual, y
+// and checkpoint: 95 us, 6.3 TB/s; the gradient with dh: 85 us, 6.3 TB/s; plain loads and stores of
+// the same bytes take 94 and 78 us). A row belongs to `tpr` threads (a multiple of 32) that hold it
+// in registers, VPT accesses of V elements each: V = 8 (16-byte accesses) when every row is aligned
+// to eight elements, V = 1 otherwise, where a warp reads 32 consecutive elements per access. In both,
+// a 32-element checkpoint block lies within a warp: four lanes of one access (V = 8) or all 32 (V = 1).
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -128,6 +129,135 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(NormArgs a) {
   }
 }
 
+// The same for many rows: a row group takes every (gridDim.x * groups)-th row, whose x and residual
+// come by one bulk copy each into a ring of stages, S rows ahead (a row lies in registers once its sum
+// is taken, and frees its stage). Three rows ahead of two groups of 4096 columns, 96 KB per SM, suffice:
+// with 192 KB (three blocks of four) 16384 x 4096 takes 118 us instead of 95.
+constexpr int kMaxGroups = 16, kRingStages = 3, kGradStages = 4;
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+
+template <bool X_BF16, bool R_BF16>
+__global__ void __launch_bounds__(512, 1) rms_norm_ring_kernel(NormArgs a) {
+  extern __shared__ __align__(128) char stages[];
+  constexpr int VPT = 2, S = kRingStages, kX = X_BF16 ? 2 : 4, kR = R_BF16 ? 2 : 4;
+  __shared__ float red[2][32];
+  __shared__ uint64_t full[kMaxGroups][S];
+  __shared__ int abort_word[2];   // a wait gave up; never set (for the last waits)
+  const int tid = threadIdx.x, tpr = blockDim.x, warps = tpr >> 5, group = threadIdx.y;
+  const int dim = (int)a.dim, nv = dim / 8;
+  const float inv_dim = 1.0f / (float)dim;
+  const int64_t step = (int64_t)gridDim.x * blockDim.y, first = (int64_t)blockIdx.x * blockDim.y + group;
+  const bool leader = tid == 0;
+  if (leader) {
+    for (int s = 0; s < S; ++s) mbar_init(&full[group][s], 1);
+    if (group == 0) abort_word[0] = abort_word[1] = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const int part = dim * (kX + (a.r ? kR : 0)), stage_bytes = part * blockDim.y;
+  char* const part0 = stages + part * group;
+  bool timed_out = false;
+  int64_t fetched = 0;   // by this thread
+  auto fetch = [&](int64_t row, int s) {
+    if (!leader || timed_out || row >= a.rows) return;
+    char* const to = part0 + s * stage_bytes;
+    uint64_t* bar = &full[group][s];
+    mbar_arrive_expect_tx(bar, (uint32_t)part);
+    ++fetched;
+    bulk_load(to, static_cast<const char*>(a.x) + row * a.xs * kX, (uint32_t)dim * kX, bar);
+    if (a.r) bulk_load(to + dim * kX, static_cast<const char*>(a.r) + row * a.rs * kR, (uint32_t)dim * kR, bar);
+  };
+  for (int s = 0; s < S; ++s) fetch(first + s * step, s);
+  float w[VPT][8];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j)
+    if (j * tpr + tid < nv) load_w<8>(a.w, a.w_bf16, (int64_t)(j * tpr + tid) * 8, w[j]);
+  int s = 0, phase = 0, parity = 0;
+#pragma unroll 1
+  for (int64_t row = first; row - group < a.rows; row += step) {
+    const bool on = row < a.rows;
+    if (on && !mbar_wait_bounded(&full[group][s], phase, abort_word, a.wait_ns ? a.wait_ns : kTimeoutNs)) {
+      timed_out = true;
+      *(volatile int*)abort_word = 1;
+    }
+    const char* const from = part0 + s * stage_bytes;
+    float h[VPT][8];
+    float2 part_sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int c = (j * tpr + tid) * 8;
+      if (on && c < dim) {
+        load8<X_BF16>(from, c, h[j]);
+        if (a.r) {
+          Raw<8, R_BF16> r;
+          r.load(from + dim * kX, c);
+          r.add(h[j]);   // h = round(h + r)
+          r.store(a.h, row * a.hs + c);
+          r.get(h[j]);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[j][e] = 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const float2 p = make_float2(h[j][e], h[j][e + 1]);
+        part_sum = __ffma2_rn(p, p, part_sum);
+      }
+    }
+    float sum = part_sum.x + part_sum.y;
+    // the row's sum; the other half of red was last read before the barrier of the row before
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (warps > 1) {
+      if ((tid & 31) == 0) red[parity][group * warps + (tid >> 5)] = sum;
+      __syncthreads();
+      sum = (tid & 31) < warps ? red[parity][group * warps + (tid & 31)] : 0.0f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      parity ^= 1;
+    }
+    // past this barrier (of the warp, if it is the group) nobody reads the stage of this row
+    fetch(row + S * step, s);
+    const float rstd = 1.0f / sqrtf(sum * inv_dim + a.eps);
+    if (on && leader) a.rstd[row] = rstd;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int c = (j * tpr + tid) * 8;
+      const bool ok = on && c < dim;
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const float2 p = __fmul2_rn(__fmul2_rn(make_float2(h[j][e], h[j][e + 1]), make_float2(rstd, rstd)),
+                                    make_float2(w[j][e], w[j][e + 1]));
+        y[e] = p.x;
+        y[e + 1] = p.y;
+      }
+      if (ok && a.y) store8<X_BF16>(a.y, row * a.ys + c, y);
+      if (a.q) {   // every lane of the warp takes part: lanes past the row count as zeros
+        uint32_t m = ok ? mx_amax8(y) : 0u;
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        if (ok) {
+          const uint32_t code = mx_scale_code(m);
+          *reinterpret_cast<uint2*>(a.q + row * a.qs + c) = mx_pack8(y, code);
+          if ((c & (kMxBlock - 1)) == 0) a.sc[row * a.scs + c / kMxBlock] = (uint8_t)code;
+        }
+      }
+    }
+    if (++s == S) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+  if (timed_out) atomicOr(a.status, kStatusTimeout);
+  if (timed_out && leader) {
+    // no copy may land after the block has gone: wait for each stage's last one
+    for (int64_t f = fetched > S ? fetched - S : 0; f < fetched; ++f)
+      mbar_wait_bounded(&full[group][f % S], (f / S) & 1, abort_word + 1, kTimeoutNs);
+  }
+}
+
 // How a row reaches the threads of the gradient:
 //   kBulk    one bulk copy per row and tensor into a ring of stages, S - 1 rows ahead (V = 8)
 //   kCopies  each thread copies its own accesses ahead, into slots that only it uses (V = 1, where
@@ -152,9 +282,6 @@ __device__ __forceinline__ void stage_element(char* slot, const void* base, int6
   else cp_async<4>(slot, static_cast<const float*>(base) + i);
 }
 
-constexpr int kGradGroups = 8, kGradStages = 4;
-constexpr uint64_t kTimeoutNs = 2000000000ull;
-
 // A row group takes every (gridDim.x * groups)-th row; each thread keeps the weight gradient of its
 // own columns in registers over all of them (in a fixed order), and the blocks' sums are added by
 // norm_dw_kernel. A row costs one block barrier, its sum's.
@@ -165,7 +292,7 @@ __global__ void __launch_bounds__(FEED == Feed::kDirect ? 1024 : 512) rms_norm_g
   constexpr int kDy = DY_BF16 ? 2 : 4, kH = H_BF16 ? 2 : 4;
   using L = GradSlot<VPT, DY_BF16, H_BF16>;
   __shared__ float red[2][32];
-  __shared__ uint64_t full[kGradGroups][kGradStages];
+  __shared__ uint64_t full[kMaxGroups][kGradStages];
   __shared__ int abort_word[2];   // a wait gave up; never set (for the last waits)
   grid_launch_dependents();
   const int tid = threadIdx.x, tpr = blockDim.x, warps = tpr >> 5, group = threadIdx.y;
@@ -404,6 +531,26 @@ bool aligned8(const void* p, int64_t stride, int bf16) {
   return (uintptr_t)p % 16 == 0 && stride % 8 == 0 && (bf16 || stride % 4 == 0);
 }
 
+constexpr int kRingSmem = 220 * 1024;   // of an SM, for the stages of its blocks
+
+// One block of 512 threads per SM, whose stages (at most 64 KB each) always fit.
+template <bool X, bool R>
+cudaError_t norm_ring(const NormArgs& a, cudaStream_t st) {
+  static PerDeviceOnce once;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = (cudaError_t)once.run(dev, [&] {
+    return (int)cudaFuncSetAttribute(rms_norm_ring_kernel<X, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
+  });
+  if (e != cudaSuccess) return e;
+  const RowShape s = row_shape(a.dim / 8, 2, 512);
+  const int64_t groups = (a.rows + s.groups - 1) / s.groups;
+  const size_t smem = (size_t)(kRingStages * s.groups * a.dim * ((X ? 2 : 4) + (a.r ? (R ? 2 : 4) : 0)));
+  rms_norm_ring_kernel<X, R><<<(unsigned)(groups < kSms ? groups : kSms), dim3(s.tpr, s.groups), smem, st>>>(a);
+  return cudaGetLastError();
+}
+
 template <int V, int VPT>
 cudaError_t norm_types(const NormArgs& a, int xb, int rb, RowShape s, cudaStream_t st) {
   const dim3 block(s.tpr, s.groups);
@@ -414,8 +561,6 @@ cudaError_t norm_types(const NormArgs& a, int xb, int rb, RowShape s, cudaStream
   else rms_norm_kernel<V, VPT, false, false><<<grid, block, 0, st>>>(a);
   return cudaGetLastError();
 }
-
-constexpr int kGradSmem = 220 * 1024;   // of an SM, for the stages of its blocks
 
 template <int V, int VPT, bool D, bool H, Feed F, int S>
 cudaError_t norm_grad_one(const NormGradArgs& a, RowShape s, int64_t stage, int per_sm, int* blocks, cudaStream_t st) {
@@ -429,24 +574,25 @@ cudaError_t norm_grad_one(const NormGradArgs& a, RowShape s, int64_t stage, int 
   if (e != cudaSuccess) return e;
   e = (cudaError_t)once.run(dev, [&] {
     return (int)cudaFuncSetAttribute(rms_norm_grad_kernel<V, VPT, D, H, F, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     kGradSmem);
+                                     kRingSmem);
   });
   if (e != cudaSuccess) return e;
   rms_norm_grad_kernel<V, VPT, D, H, F, S><<<*blocks, dim3(s.tpr, s.groups), smem, st>>>(a);
   return cudaGetLastError();
 }
 
-// Blocks of 256 threads, two per SM, or one of 512; rows ahead as their stages leave room for.
+// Blocks of 256 threads (512 for the longest rows), two per SM where their four stages leave room
+// (4096 columns of fp32 with dh, one block with four stages or two with two: 84 and 91 us for 8192
+// rows; bf16, 16384 rows, two with four, one with four, two with two: 85, 121 and 116 us).
 template <int V, int VPT, bool D, bool H, Feed F>
 cudaError_t norm_grad_stages(const NormGradArgs& a, int* blocks, cudaStream_t st) {
   const RowShape s = row_shape(a.dim / V, VPT, 256);
-  const int per_sm = s.tpr <= 256 ? 2 : 1;
   const int64_t stage = F == Feed::kBulk
                             ? s.groups * a.dim * ((D ? 2 : 4) + (a.dh ? 2 : 1) * (H ? 2 : 4))
                             : s.groups * s.tpr * (a.dh ? GradSlot<VPT, D, H>::kPitchDh : GradSlot<VPT, D, H>::kPitch);
-  if (stage * kGradStages * per_sm <= kGradSmem)
-    return norm_grad_one<V, VPT, D, H, F, kGradStages>(a, s, stage, per_sm, blocks, st);
-  return norm_grad_one<V, VPT, D, H, F, 2>(a, s, stage, per_sm, blocks, st);
+  const int64_t fit = kRingSmem / (kGradStages * stage), most = s.tpr <= 256 ? 2 : 1;
+  if (fit >= 1) return norm_grad_one<V, VPT, D, H, F, kGradStages>(a, s, stage, (int)(fit < most ? fit : most), blocks, st);
+  return norm_grad_one<V, VPT, D, H, F, 2>(a, s, stage, 1, blocks, st);
 }
 
 template <bool D, bool H>
@@ -471,6 +617,13 @@ cudaError_t launch_rms_norm(const NormArgs& a, int x_bf16, int r_bf16, int sms, 
                   (!a.r || (aligned8(a.r, a.rs, r_bf16) && aligned8(a.h, a.hs, r_bf16))) &&
                   (!a.y || aligned8(a.y, a.ys, x_bf16)) &&
                   (!a.q || ((uintptr_t)a.q % 8 == 0 && a.qs % 8 == 0));
+  // from 2^22 elements on the ring is no slower (us, bf16 with residual, y and checkpoint, ring and
+  // not: 1024 x 4096 10.0 and 9.9, 4096 x 4096 27 and 32, 16384 x 4096 93 and 112, 1024 x 8192 15 and
+  // 19); below, starting it costs up to 1 us more (64 x 4096 3.6 and 2.9)
+  if (v8 && a.dim <= 8192 && a.rows * a.dim >= (int64_t(1) << 22)) {
+    if (x_bf16) return r_bf16 ? norm_ring<true, true>(a, st) : norm_ring<true, false>(a, st);
+    return r_bf16 ? norm_ring<false, true>(a, st) : norm_ring<false, false>(a, st);
+  }
   if (v8) {
     const RowShape s = row_shape(a.dim / 8, a.rows < 2 * sms ? 1 : 2, 128);
     if (s.vpt <= 1) return norm_types<8, 1>(a, x_bf16, r_bf16, s, st);

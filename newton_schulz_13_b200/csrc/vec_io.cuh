@@ -71,6 +71,18 @@ struct Raw<8, true> {
       v[2 * i + 1] = f.y;
     }
   }
+  // adds v in fp32 and rounds
+  __device__ __forceinline__ void add(const float (&v)[8]) {
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __fadd2_rn(make_float2(v[2 * i], v[2 * i + 1]), __bfloat1622float2(h[i]));
+      h[i] = __floats2bfloat162_rn(f.x, f.y);
+    }
+  }
+  __device__ __forceinline__ void store(void* p, int64_t i) const {
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + i) = r;
+  }
 };
 template <>
 struct Raw<8, false> {
@@ -83,6 +95,15 @@ struct Raw<8, false> {
   __device__ __forceinline__ void get(float (&v)[8]) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+  __device__ __forceinline__ void add(const float (&v)[8]) {
+    a = make_float4(a.x + v[0], a.y + v[1], a.z + v[2], a.w + v[3]);
+    b = make_float4(b.x + v[4], b.y + v[5], b.z + v[6], b.w + v[7]);
+  }
+  __device__ __forceinline__ void store(void* p, int64_t i) const {
+    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+    q[0] = a;
+    q[1] = b;
   }
 };
 template <>

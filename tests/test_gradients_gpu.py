@@ -416,6 +416,60 @@ def test_rms_norm_grad_against_differences():
     assert abs((dweight.double() * dw_dir).sum().item() - num_w) <= mag_w * (SUM * E + 2.0 ** -52 * 1920 / s)
 
 
+@pytest.mark.parametrize("rows,dim", [(4096, 4096), (9000, 520), (2000, 8192)])
+def test_rms_norm_wait_limit(rows, dim):
+    """With a limit of 1 ns a call either reports that a wait for a row ran out or, where every row
+    was there in time, is right; the device stays usable."""
+    import newton_schulz_13_b200 as ns
+    x, r, w = normal((rows, dim), BF16, 57), normal((rows, dim), BF16, 58), torch.ones(dim, device="cuda")
+    want = ns.rms_norm(x, w, residual=r, checkpoint=True)
+    grad = ns.rms_norm_grad(x, want.h, w, want.rstd, dh=r)
+    assert ns.check_status() == ns.OK
+    out_of_cache = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for call, right in ((lambda: ns.rms_norm(x, w, residual=r, checkpoint=True)[:3], want[:3]),
+                        (lambda: ns.rms_norm_grad(x, want.h, w, want.rstd, dh=r), grad)):
+        for _ in range(5):
+            out_of_cache.zero_()
+            ns.set_wait_limit_ns(1)
+            try:
+                got = call()
+                try:
+                    assert ns.check_status() == ns.OK
+                    assert all(torch.equal(a, b) for a, b in zip(got, right))
+                    print("no wait ran out")
+                except ns.MuonError as e:
+                    assert e.code == ns.ERR_TIMEOUT
+                    print("reported")
+            finally:
+                ns.set_wait_limit_ns(0)
+    again = ns.rms_norm(x, w, residual=r, checkpoint=True)
+    assert torch.equal(again.y, want.y) and torch.equal(again.checkpoint.q.view(torch.uint8), want.checkpoint.q.view(torch.uint8))
+    assert all(torch.equal(a, b) for a, b in zip(ns.rms_norm_grad(x, want.h, w, want.rstd, dh=r), grad))
+    assert ns.check_status() == ns.OK
+
+
+@pytest.mark.parametrize("x_dt,r_dt", [(BF16, BF16), (BF16, FP32), (FP32, BF16), (FP32, FP32), (BF16, None)])
+@pytest.mark.parametrize("rows,dim", [(66000, 64), (17000, 264), (5462, 768), (1031, 4096), (600, 8192)])
+def test_rms_norm_many_rows(rows, dim, x_dt, r_dt):
+    """Sizes at which rows come through the ring, in shapes that leave its last groups idle."""
+    import newton_schulz_13_b200 as ns
+    x = normal((rows, dim), x_dt, 47)
+    r = None if r_dt is None else normal((rows, dim), r_dt, 48, 2.0)
+    w = 1.0 + 0.1 * torch.randn(dim, generator=gen(49), device="cuda")
+    got = ns.rms_norm(strided(x, 8, 8), w, residual=r, eps=1e-5, checkpoint=True)
+    want_h, want_rstd, want = norm_want(x, r, w, 1e-5)
+    assert torch.equal(got.h, want_h)
+    within(got.rstd, want_rstd, want_rstd * SUM * E, "rstd")
+    within(got.y, want, want.abs() * (SUM * E + U[x_dt]), "y")
+    back = ns.checkpoint_restore(got.checkpoint, dtype=FP32)
+    each = got.checkpoint.scales.double().repeat_interleave(32, 1)[:, :dim]
+    within(back, want, want.abs() * (2.0 ** -4 + SUM * E) + each * 2.0 ** -10, "checkpoint")
+    xi, ri = x.clone(), None if r is None else r.clone()
+    same = ns.rms_norm(xi, w, residual=ri, h=ri, y=xi, checkpoint=True)      # in place
+    assert torch.equal(same.y, got.y) and (r is None or torch.equal(ri, got.h))
+    assert ns.check_status() == ns.OK
+
+
 # ---------------------------------------------------------------------------- weight gradient
 
 WGRAD = [(0, 5, 40), (1, 1, 1), (1, 256, 256), (15, 48, 1536), (63, 80, 33), (64, 257, 300), (65, 256, 512), (130, 1536, 48),
