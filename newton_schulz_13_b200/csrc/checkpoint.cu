@@ -8,6 +8,7 @@
 
 #include "mx.cuh"
 #include "ops_internal.h"
+#include "ptx.cuh"
 #include "vec_io.cuh"
 
 namespace muon {
@@ -79,8 +80,15 @@ __global__ void __launch_bounds__(kThreads) mx_store_any_kernel(MxArgs a, Div pe
   }
 }
 
+__device__ __forceinline__ void zero_words(const MxArgs& a) {
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < a.zeros; i += kThreads) a.zero[i] = 0;
+}
+
 template <bool O_BF16>
 __global__ void __launch_bounds__(kThreads) mx_restore_kernel(MxArgs a, Div per_row, uint32_t total) {
+  grid_launch_dependents();
+  zero_words(a);
   const uint32_t t0 = blockIdx.x * (kAcc * kThreads) + threadIdx.x;
   uint2 raw[kAcc];
   uint32_t row[kAcc], c[kAcc], code[kAcc];
@@ -110,6 +118,8 @@ __global__ void __launch_bounds__(kThreads) mx_restore_kernel(MxArgs a, Div per_
 
 template <bool O_BF16>
 __global__ void __launch_bounds__(kThreads) mx_restore_any_kernel(MxArgs a, Div per_row, uint32_t total) {
+  grid_launch_dependents();
+  zero_words(a);
   const int lane = threadIdx.x & 31;
   const uint32_t b = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);   // a 32-element block
   if (b < total) {

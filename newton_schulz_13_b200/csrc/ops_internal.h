@@ -82,6 +82,8 @@ struct MxArgs {
   uint8_t* q;
   uint8_t* sc;
   int64_t rows, dim, xs, qs, scs;
+  uint32_t* zero;       // restore: `zeros` words that the first block also sets to 0
+  int zeros;
 };
 cudaError_t launch_mx_store(const MxArgs& a, int x_bf16, cudaStream_t s);
 cudaError_t launch_mx_restore(const MxArgs& a, int out_bf16, cudaStream_t s);

@@ -30,6 +30,19 @@ __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// ---------------------------------------------------------------- registers
+// The calling group of four warps gives registers back, or takes more of those the block was
+// launched with (N per thread from now on; waits until they are free).
+template <uint32_t N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <uint32_t N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // ---------------------------------------------------------------- per-thread asynchronous copies
 // global -> shared, 4 bytes or 16 (both sides aligned to the size); the thread that issued a copy
 // sees it after cp_async_wait, no other thread does.

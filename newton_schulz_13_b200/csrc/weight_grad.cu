@@ -2,19 +2,21 @@
 // with x the checkpoint's values (mx.cuh), which are exact in bf16. Compute-bound: 2 rows n k FLOPs
 // on the tcgen05 tensor cores.
 //
-// Three launches:
+// Two launches:
 //   stage    x (and dy, when its rows are not 16-byte aligned or it is fp32) written to the
 //            workspace as bf16. An fp32 dy becomes three bf16 planes whose sum is dy exactly
-//            (8 + 8 + 8 mantissa bits, by truncation), contracted one after the other, so nothing
-//            of it is lost.
+//            (8 + 8 + 8 mantissa bits, by truncation), so nothing of it is lost.
 //   product  CTA pairs (cta_group::2) on 256 x 256 tiles; both operands are MN-major (the
-//            contraction runs over rows t). Warp 0 loads 64-row slices with TMA, warp 1 of the even
-//            CTA issues the MMAs, eight warps drain the accumulator. The accumulator is drained
-//            every kChunk slices (1024 rows) into registers and added there in fp32: the tensor
-//            core truncates its running sum at every step, a bias that grows with the number of
-//            steps.
-//   reduce   where the rows are split over several units of a tile (few tiles, many rows): the
-//            parts, in fp32 in the workspace, are added in order.
+//            contraction runs over rows t). Warp 0 loads 64-row slices with TMA (one of x, one of
+//            each plane of dy), warp 1 of the even CTA issues the MMAs, eight warps drain the
+//            accumulator. The accumulator is drained every 1024 rows (of one plane) into registers
+//            and added there in fp32: the tensor core truncates its running sum at every step, a
+//            bias that grows with the number of steps.
+//            Whole tiles go to the pairs in rounds; the slices of the tiles left over after the
+//            last full round are dealt out evenly. Where a tile so falls to several pairs, the one
+//            with its last slices adds the others' sums, which come through the workspace in fp32,
+//            to its own, always in the same order. It waits only for pairs of lower numbers, whose
+//            blocks start no later than its own, and for work that they do first.
 // Waits are bounded as in the Newton-Schulz products (pair_pipe.cuh describes the unwinding).
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -33,65 +35,172 @@ namespace {
 
 constexpr int kTile = 256;                      // grad rows and columns per CTA pair
 constexpr int kSlice = 64;                      // contraction rows per pipeline stage
-constexpr int kChunk = 16;                      // slices between drains of the accumulator
-constexpr int kStages = 6;
 constexpr uint32_t kBox = 64 * 64 * 2;          // 64 contraction rows x 64 columns, bf16
 constexpr uint32_t kOperand = 2 * kBox;         // a CTA's 128 columns of one operand
-constexpr uint32_t kStage = 2 * kOperand;
+constexpr uint32_t kRing = 12 * kOperand;       // operand stages: 6 of x and dy, or 3 of x and three planes
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr uint32_t kTransposeFloats = 32 * 33;  // per epilogue warp
-constexpr size_t kSmem = 1024 + kStages * kStage + kEpiWarps * kTransposeFloats * 4 + 256;
+constexpr int kEpiFirst = 4;                    // warps 2 and 3 are idle: registers go by groups of four warps
+constexpr int kThreads = 32 * (kEpiFirst + kEpiWarps);
+// Registers per thread: 384 threads launch with at most 168; the first four warps hand most of
+// theirs to the eight that hold 128 sums each (72 + 2 x 216 = 3 x 168).
+constexpr uint32_t kRegsFew = 72, kRegsMany = 216;
+constexpr uint32_t kTranspose = 32 * 32 * 4;    // bytes per epilogue warp
+constexpr size_t kSmem = 1024 + kRing + kEpiWarps * kTranspose + 512;
 static_assert(kSmem <= 232448, "dynamic shared memory per CTA");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr int64_t kCost = 8;                    // see layout_of
 constexpr uint32_t kGroup = 8;                  // tile rows that sweep the columns together (L2 reuse)
 
+constexpr int64_t kPart = kTile * kTile;        // floats of one part
+constexpr uint32_t kPiece = 32 * 64 * 4, kJoin = 3;   // bytes of a warp's 64 columns of a part, and pieces ahead
+static_assert(kJoin * kPiece * kEpiWarps <= kRing, "join");
+
 struct ProductArgs {
-  void* grad;               // the output, or (splits > 1) the fp32 parts [splits][n][k]
+  void* grad;
   int64_t gs;               // its row stride
-  uint32_t n, k, tiles_n, tiles_k, splits;
-  uint32_t slices;          // slices of one plane of dy
-  uint32_t planes;
+  float* parts;             // [workers + left - 1][kPart]
+  uint32_t* ready;          // [left][16]: parts written of each left-over tile, by epilogue warp of the pair
+  uint32_t n, k, tiles_n, tiles_k;
+  uint32_t whole, left;     // tiles given to the pairs whole, and the rest, whose slices are dealt out
+  uint32_t workers;         // pairs that share them: each has `share` slices, the first `extra` one more
+  uint32_t share, extra;
+  uint32_t slices;
   uint32_t plane_rows;      // rows between planes of dy
   int accumulate;
+  int vec;                  // groups of four columns of grad are aligned
   int* status;
   uint64_t wait_ns;
 };
 
-// Unit u of a launch: a tile and its range [s0, s1) of the planes * slices contraction slices.
-struct Unit {
-  uint32_t ti, tj, s0, s1, split;
-};
-
-__host__ __device__ inline Unit unit_of(const ProductArgs& a, uint32_t u) {
-  const uint32_t tiles = a.tiles_n * a.tiles_k, all = a.slices * a.planes;
-  Unit r;
-  r.split = u / tiles;
-  const uint32_t t = u - r.split * tiles;
-  const uint32_t per = kGroup * a.tiles_k, g = t / per, first = g * kGroup;
-  const uint32_t size = a.tiles_n - first < kGroup ? a.tiles_n - first : kGroup;
-  r.ti = first + (t - g * per) % size;
-  r.tj = (t - g * per) / size;
-  r.s0 = (uint32_t)((uint64_t)all * r.split / a.splits);
-  r.s1 = (uint32_t)((uint64_t)all * (r.split + 1) / a.splits);
-  return r;
+// Four consecutive, aligned columns of grad.
+template <bool BF16>
+__device__ __forceinline__ float4 load4(const void* p, int64_t at) {
+  if constexpr (BF16) {
+    const uint2 raw = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + at);
+    return make_float4(__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u),
+                       __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u));
+  } else {
+    return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+  }
 }
 
-template <bool OUT_BF16>
+template <bool BF16>
+__device__ __forceinline__ void store4(void* p, int64_t at, const float4& f) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(f.x, f.y), b = __floats2bfloat162_rn(f.z, f.w);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + at) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  } else {
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = f;
+  }
+}
+
+// An epilogue warp's 32 rows x 32 columns of grad (rows x cols of them exist) go through its 4 KB of
+// shared memory. 16-byte chunk c of row r lies at chunk c ^ (r & 7) of its row: eight lanes that
+// have a row's 32 columns, and lanes that each have a row, meet no bank twice. `at` is the place of
+// the first row and column.
+template <bool BF16>
+__device__ __forceinline__ void block_in_any(const ProductArgs& a, int64_t at, int rows, int cols, int lane, float4* stg) {
+#pragma unroll 1
+  for (int r = 0; r < 32; ++r)
+    reinterpret_cast<float*>(stg + r * 8 + ((lane >> 2) ^ (r & 7)))[lane & 3] =
+        r < rows && lane < cols ? load1<BF16>(a.grad, at + r * a.gs + lane) : 0.0f;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void block_out(const ProductArgs& a, int64_t at, int rows, int cols, bool fast, int lane,
+                                          const float4* stg) {
+  if (fast) {
+    const int sub = lane >> 3, chunk = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      store4<BF16>(a.grad, at + (4 * i + sub) * a.gs + chunk * 4, stg[(4 * i + sub) * 8 + (chunk ^ ((4 * i + sub) & 7))]);
+  } else if (lane < cols) {
+#pragma unroll 1
+    for (int r = 0; r < rows; ++r)
+      store1<BF16>(a.grad, at + r * a.gs + lane, reinterpret_cast<const float*>(stg + r * 8 + ((lane >> 2) ^ (r & 7)))[lane & 3]);
+  }
+}
+
+// A tile and its range [s0, s1) of slices. part: where its sum goes among the parts, or -1: to
+// grad, after `others` parts of the tile from `first_part` on.
+struct Unit {
+  uint32_t ti, tj, s0, s1, left_tile, others, first_part;
+  int part;
+};
+
+// The units of one pair, in the order in which all of its warps take them: whole tiles, then, as
+// worker q, its slices of the left-over tiles laid end to end (below 2^31 in all), last tile first.
+// Its part of left-over tile t has place q + t, which no other pair and tile have.
+struct Units {
+  const ProductArgs& a;
+  uint32_t next_whole, pairs, q;
+  uint32_t begin, at;
+  __device__ Units(const ProductArgs& a_, uint32_t pair, uint32_t pairs_) : a(a_), next_whole(pair), pairs(pairs_), q(pair) {
+    begin = at = 0;
+    if (pair < a.workers) {
+      begin = pair * a.share + min(pair, a.extra);
+      at = begin + a.share + (pair < a.extra ? 1 : 0);
+    }
+  }
+  __device__ bool next(Unit& u) {
+    uint32_t tile;
+    u.s0 = 0;
+    u.s1 = a.slices;
+    u.part = -1;
+    u.others = 0;
+    if (next_whole < a.whole) {
+      tile = next_whole;
+      next_whole += pairs;
+    } else if (at > begin) {
+      const uint32_t t = (at - 1) / a.slices, t0 = t * a.slices;
+      u.s0 = begin > t0 ? begin - t0 : 0;
+      u.s1 = at - t0;
+      at = t0 + u.s0;
+      tile = a.whole + t;
+      u.left_tile = t;
+      if (u.s1 < a.slices) {
+        u.part = (int)(q + t);
+      } else if (u.s0 > 0) {
+        const uint32_t more = a.extra * (a.share + 1);   // slices of the workers that have one more
+        const uint32_t q0 = t0 < more ? t0 / (a.share + 1) : a.extra + (t0 - more) / a.share;   // has the tile's first
+        u.others = q - q0;
+        u.first_part = q0 + t;
+      }
+    } else {
+      return false;
+    }
+    tile_place(a.tiles_n, a.tiles_k, tile, u.ti, u.tj);
+    return true;
+  }
+  static __device__ void tile_place(uint32_t tiles_n, uint32_t tiles_k, uint32_t tile, uint32_t& ti, uint32_t& tj) {
+    const uint32_t per = kGroup * tiles_k, g = tile / per, first = g * kGroup;
+    const uint32_t size = min(kGroup, tiles_n - first);
+    ti = first + (tile - g * per) % size;
+    tj = (tile - g * per) / size;
+  }
+};
+
+template <bool OUT_BF16, int PLANES>
 __global__ void __launch_bounds__(kThreads, 1)
     wgrad_product_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_x,
                          const ProductArgs a) {
+  constexpr int kStages = PLANES == 1 ? 6 : 3;
+  constexpr uint32_t kStage = (1 + PLANES) * kOperand;   // x, then the planes of dy
+  constexpr uint32_t kChunk = 16 / PLANES;               // slices between drains: at most 64 steps
+  static_assert(kStages * kStage == kRing, "stages");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  float* transpose = reinterpret_cast<float*>(smem + kStages * kStage);
-  uint64_t* full = reinterpret_cast<uint64_t*>(transpose + kEpiWarps * kTransposeFloats);
+  float4* transpose = reinterpret_cast<float4*>(smem + kRing);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRing + kEpiWarps * kTranspose);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* join = drain + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(join + kEpiWarps * kJoin);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* zero_flag = abort_flag + 1;   // never set: the drain waits poll it
   volatile uint32_t* fill_count = reinterpret_cast<volatile uint32_t*>(zero_flag + 1);
@@ -100,7 +209,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const uint32_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
-  const uint32_t units = a.tiles_n * a.tiles_k * a.splits;
   const uint64_t wait_ns = a.wait_ns ? a.wait_ns : kTimeoutNs;
 
   if (threadIdx.x == 0) {
@@ -113,6 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&tempty[i], 2 * kEpiWarps);
     }
     mbar_init(drain, 1);
+    for (uint32_t i = 0; i < kEpiWarps * kJoin; ++i) mbar_init(&join[i], 1);
     *abort_flag = 0;
     *zero_flag = 0;
     *fill_count = 0;
@@ -131,26 +240,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_launch_dependents();
 
   bool timed_out = false;
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < kEpiFirst) {
+    regs_dec<kRegsFew>();
+    if (warp == 0 && lane == 0) {
       uint32_t stage = 0, phase = 0, fills = 0;
-      for (uint32_t u = pair; u < units && !timed_out; u += pairs) {
-        const Unit w = unit_of(a, u);
+      Units units(a, pair, pairs);
+      Unit w;
+      while (!timed_out && units.next(w)) {
         const int32_t n0 = (int32_t)(w.ti * kTile + rank * 128), k0 = (int32_t)(w.tj * kTile + rank * 128);
         for (uint32_t s = w.s0; s < w.s1; ++s) {
           if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, wait_ns)) {
             timed_out = true;
             break;
           }
-          const uint32_t plane = s / a.slices, t0 = (s - plane * a.slices) * kSlice;
-          const int32_t yd = (int32_t)(plane * a.plane_rows + t0), yx = (int32_t)t0;
+          const int32_t t0 = (int32_t)(s * kSlice);
           uint8_t* dst = smem + stage * kStage;
           const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
           if (leader) mbar_arrive_expect_tx(&full[stage], 2 * kStage);
-          tma_load_2d_pair(dst, &map_dy, bar, n0, yd);
-          tma_load_2d_pair(dst + kBox, &map_dy, bar, n0 + 64, yd);
-          tma_load_2d_pair(dst + kOperand, &map_x, bar, k0, yx);
-          tma_load_2d_pair(dst + kOperand + kBox, &map_x, bar, k0 + 64, yx);
+          tma_load_2d_pair(dst, &map_x, bar, k0, t0);
+          tma_load_2d_pair(dst + kBox, &map_x, bar, k0 + 64, t0);
+#pragma unroll
+          for (int p = 0; p < PLANES; ++p) {
+            const int32_t y = t0 + (int32_t)(p * a.plane_rows);
+            tma_load_2d_pair(dst + (1 + p) * kOperand, &map_dy, bar, n0, y);
+            tma_load_2d_pair(dst + (1 + p) * kOperand + kBox, &map_dy, bar, n0 + 64, y);
+          }
           ++fills;
           if (++stage == kStages) { stage = 0; phase ^= 1u; }
         }
@@ -158,13 +272,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (timed_out) raise_abort(abort_flag, true, rank);
       *fill_count = fills;
     }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (warp == 1 && lane == 0 && leader) {
       const uint32_t idesc = idesc_bf16_f32(kTile, kTile, 1, 1);
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
-      for (uint32_t u = pair; u < units && !timed_out; u += pairs) {
-        const Unit w = unit_of(a, u);
+      Units units(a, pair, pairs);
+      Unit w;
+      while (!timed_out && units.next(w)) {
         for (uint32_t c0 = w.s0; c0 < w.s1 && !timed_out; c0 += kChunk) {
           if (!mbar_wait_bounded(&tempty[acc], acc_phase ^ 1u, abort_flag, wait_ns)) {
             timed_out = true;
@@ -178,11 +291,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             }
             tc_fence_after();
-            const uint32_t ad = smem_u32(smem + stage * kStage), bd = ad + kOperand;
+            const uint32_t bd = smem_u32(smem + stage * kStage), ad = bd + kOperand;
 #pragma unroll
-            for (uint32_t i = 0; i < kSlice / 16; ++i)
-              tc_mma_f16_pair(tmem_base + acc * 256u, smem_desc_sw128(ad + i * 2048u, kBox, 1024),
-                              smem_desc_sw128(bd + i * 2048u, kBox, 1024), idesc, s != c0 || i != 0 ? 1u : 0u);
+            for (uint32_t p = 0; p < PLANES; ++p)
+#pragma unroll
+              for (uint32_t i = 0; i < kSlice / 16; ++i)
+                tc_mma_f16_pair(tmem_base + acc * 256u, smem_desc_sw128(ad + p * kOperand + i * 2048u, kBox, 1024),
+                                smem_desc_sw128(bd + i * 2048u, kBox, 1024), idesc, s != c0 || p != 0 || i != 0 ? 1u : 0u);
             tc_commit_pair_mc(&empty[stage], 0x3);
             if (++stage == kStages) { stage = 0; phase ^= 1u; }
           }
@@ -197,15 +312,65 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
+    regs_inc<kRegsMany>();
     // each warp: 32 accumulator rows (a lane each) x 128 of the tile's columns
-    const uint32_t quarter = (uint32_t)(warp & 3), half = (uint32_t)(warp - 2) >> 2;
-    float* stg = transpose + (uint32_t)(warp - 2) * kTransposeFloats;
+    const uint32_t quarter = (uint32_t)(warp & 3), half = (uint32_t)(warp - kEpiFirst) >> 2;
+    float4* stg = transpose + (uint32_t)(warp - kEpiFirst) * 256;
     uint32_t acc = 0, acc_phase = 0;
-    for (uint32_t u = pair; u < units; u += pairs) {
-      const Unit w = unit_of(a, u);
+    Units units(a, pair, pairs);
+    Unit w;
+    while (units.next(w)) {
+      const int64_t r0 = (int64_t)w.ti * kTile + rank * 128 + quarter * 32, col0 = (int64_t)w.tj * kTile + half * 128;
+      const int rows = (int)min((int64_t)32, max((int64_t)0, (int64_t)a.n - r0));
+      auto block = [&](int g, int& cols, bool& fast) {
+        cols = (int)min((int64_t)32, max((int64_t)0, (int64_t)a.k - col0 - g * 32));
+        fast = a.vec && rows == 32 && cols == 32;
+        return r0 * a.gs + col0 + g * 32;
+      };
+      // the sums begin with the old gradient, whose way here the first MMAs hide
       float sum[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) sum[i] = 0.0f;
+      if (a.accumulate && w.part < 0) {
+        const int sub = lane >> 3, chunk = lane & 7;
+        const bool all_fast = a.vec && rows == 32 && col0 + 128 <= (int64_t)a.k;
+        if (all_fast) {   // all loads first: rows 4 i + sub, columns 32 g + 4 chunk on
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 v = load4<OUT_BF16>(a.grad, r0 * a.gs + col0 + g * 32 + (4 * i + sub) * a.gs + chunk * 4);
+              sum[g * 32 + i * 4] = v.x;
+              sum[g * 32 + i * 4 + 1] = v.y;
+              sum[g * 32 + i * 4 + 2] = v.z;
+              sum[g * 32 + i * 4 + 3] = v.w;
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          int cols;
+          bool fast;
+          const int64_t at = block(g, cols, fast);
+          __syncwarp();
+          if (all_fast) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              stg[(4 * i + sub) * 8 + (chunk ^ ((4 * i + sub) & 7))] =
+                  make_float4(sum[g * 32 + i * 4], sum[g * 32 + i * 4 + 1], sum[g * 32 + i * 4 + 2], sum[g * 32 + i * 4 + 3]);
+          } else {
+            block_in_any<OUT_BF16>(a, at, rows, cols, lane, stg);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float4 v = stg[lane * 8 + (c ^ (lane & 7))];
+            sum[g * 32 + c * 4] = v.x;
+            sum[g * 32 + c * 4 + 1] = v.y;
+            sum[g * 32 + c * 4 + 2] = v.z;
+            sum[g * 32 + c * 4 + 3] = v.w;
+          }
+        }
+      }
       for (uint32_t c0 = w.s0; c0 < w.s1; c0 += kChunk) {
         if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, wait_ns))) {
           timed_out = true;
@@ -227,29 +392,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
       if (timed_out) break;
-      const int64_t r0 = (int64_t)w.ti * kTile + rank * 128 + quarter * 32;
-      const int64_t base = a.splits > 1 ? (int64_t)w.split * a.n * a.k : 0;
+      const uint32_t me = rank * 8 + quarter * 2 + half;   // among the pair's epilogue warps
+      if (w.part >= 0) {
+        // four columns of the warp's 32 rows together
+        float4* out = reinterpret_cast<float4*>(a.parts + w.part * kPart + me * 4096) + lane;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int64_t col = (int64_t)w.tj * kTile + half * 128 + g * 32 + lane;
+        for (int i = 0; i < 32; ++i) out[i * 32] = make_float4(sum[i * 4], sum[i * 4 + 1], sum[i * 4 + 2], sum[i * 4 + 3]);
+        __threadfence();
         __syncwarp();
+        if (lane == 0) red_release_gpu_add(a.ready + w.left_tile * 16 + me, 1);
+        continue;
+      }
+      if (w.others) {
+        // the last unit of the pair: the operand ring is free, and brings the parts in pieces of
+        // 64 columns, kJoin of them ahead
+        const float* from = a.parts + w.first_part * kPart + me * 4096;
+        uint8_t* slots = smem + (uint32_t)(warp - kEpiFirst) * (kRing / kEpiWarps);
+        uint64_t* landed = join + (warp - kEpiFirst) * kJoin;
+        bool ok = lane != 0 || counter_wait_bounded(a.ready + w.left_tile * 16 + me, w.others, abort_flag, wait_ns);
+        fence_proxy_async_global();
+        const uint32_t pieces = w.others * 2;
+        auto fetch = [&](uint32_t i) {
+          if (lane != 0 || i >= pieces) return;
+          uint64_t* bar = landed + i % kJoin;
+          mbar_arrive_expect_tx(bar, kPiece);
+          bulk_load(slots + i % kJoin * kPiece, from + (i >> 1) * kPart + (i & 1) * 2048, kPiece, bar);
+        };
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok)
+          for (uint32_t i = 0; i < kJoin; ++i) fetch(i);
+        for (uint32_t i = 0; ok && i < pieces; i += 2) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) stg[lane * 33 + i] = sum[g * 32 + i];
-        __syncwarp();
-        if (col < (int64_t)a.k) {
-          const int rows = (int)min((int64_t)32, max((int64_t)0, (int64_t)a.n - r0));
-#pragma unroll 8
-          for (int r = 0; r < rows; ++r) {
-            const int64_t at = base + (r0 + r) * a.gs + col;
-            float v = stg[r * 33 + lane];
-            if (a.splits > 1) {
-              static_cast<float*>(a.grad)[at] = v;
-            } else {
-              if (a.accumulate) v += load1<OUT_BF16>(a.grad, at);
-              store1<OUT_BF16>(a.grad, at, v);
+          for (uint32_t h = 0; h < 2; ++h) {
+            // a copy that was asked for is waited for with the long limit: it must not land later
+            if (!mbar_wait_bounded(landed + (i + h) % kJoin, (i + h) / kJoin & 1, zero_flag, kTimeoutNs)) timed_out = true;
+            const float4* p = reinterpret_cast<const float4*>(slots + (i + h) % kJoin * kPiece) + lane;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const float4 v = p[c * 32];
+              sum[h * 64 + c * 4] += v.x;
+              sum[h * 64 + c * 4 + 1] += v.y;
+              sum[h * 64 + c * 4 + 2] += v.z;
+              sum[h * 64 + c * 4 + 3] += v.w;
             }
+            __syncwarp();
+            fetch(i + h + kJoin);
           }
         }
+        if (!ok) {
+          timed_out = true;
+          break;
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        int cols;
+        bool fast;
+        const int64_t at = block(g, cols, fast);
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          stg[lane * 8 + (c ^ (lane & 7))] = make_float4(sum[g * 32 + c * 4], sum[g * 32 + c * 4 + 1],
+                                                         sum[g * 32 + c * 4 + 2], sum[g * 32 + c * 4 + 3]);
+        __syncwarp();
+        block_out<OUT_BF16>(a, at, rows, cols, fast, lane, stg);
       }
     }
     if (timed_out && lane == 0) raise_abort(abort_flag, true, rank);
@@ -270,19 +476,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc_pair(tmem_base, kTmemCols);
 }
 
-// grad (+)= the sum of the parts in order (zero parts: grad becomes 0).
+// rows = 0: the empty sum.
 template <bool OUT_BF16>
-__global__ void __launch_bounds__(256) wgrad_reduce_kernel(const float* __restrict__ parts, void* grad, int64_t gs,
-                                                           int64_t n, int64_t k, int splits, int accumulate) {
-  grid_dependency_wait();
-  const int64_t total = n * k;
-  for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += (int64_t)gridDim.x * 256) {
-    const int64_t r = t / k, at = r * gs + (t - r * k);
-    float v = 0.0f;
-    for (int s = 0; s < splits; ++s) v += parts[s * total + t];
-    if (accumulate) v += load1<OUT_BF16>(grad, at);
-    store1<OUT_BF16>(grad, at, v);
-  }
+__global__ void __launch_bounds__(256) wgrad_zero_kernel(void* grad, int64_t gs, int64_t n, int64_t k) {
+  for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < n * k; t += (int64_t)gridDim.x * 256)
+    store1<OUT_BF16>(grad, t / k * gs + t % k, 0.0f);
 }
 
 // Copies dy into bf16 rows of `pitch` elements; an fp32 dy into three planes, plane_rows apart.
@@ -335,9 +533,10 @@ cudaError_t operand_map(CUtensorMap* map, const void* base, int64_t rows, int64_
 }
 
 struct Layout {
-  int64_t x, dy, parts, bytes;    // workspace offsets
+  int64_t x, dy, parts, ready, bytes;    // workspace offsets
   int64_t x_pitch, dy_pitch;
-  int planes, splits;
+  int planes;
+  uint32_t tiles_n, tiles_k, slices, whole, left, workers;
   bool copy_dy;
 };
 
@@ -349,48 +548,46 @@ Layout layout_of(int64_t rows, int64_t n, int64_t k, int dy_bf16, int dy_aligned
   l.copy_dy = !dy_bf16 || !dy_aligned;
   l.x_pitch = up(k, 8);
   l.dy_pitch = up(n, 8);
-  // splits of the contraction: rounds of units over the pairs x slices per unit, plus the parts'
-  // way through memory, all in units of one slice's time (about 0.3 us; 1.2 MB of traffic)
-  const int64_t tiles = (n + kTile - 1) / kTile * ((k + kTile - 1) / kTile), pairs = kSms / 2;
-  const int64_t slices = (rows + kSlice - 1) / kSlice * l.planes;
-  double best = 0;
-  l.splits = 1;
-  for (int64_t s = 1; s <= 64 && s <= slices; ++s) {
-    const double rounds = (double)((tiles * s + pairs - 1) / pairs);
-    double cost = rounds * ((double)((slices + s - 1) / s) + 4.0);
-    if (s > 1) cost += 8.0 + 8.0 * (double)s * n * k / 1.2e6;
-    if (s == 1 || cost < best) {
+  l.tiles_n = (uint32_t)((n + kTile - 1) / kTile);
+  l.tiles_k = (uint32_t)((k + kTile - 1) / kTile);
+  l.slices = (uint32_t)((rows + kSlice - 1) / kSlice);
+  // The tiles of the last round whole, or dealt out to so many workers that the last of them ends
+  // soonest, in slices of one plane (0.33 us each): its slices, 4 for each part that it adds (1.3 us)
+  // and kCost for the joining.
+  const int64_t tiles = (int64_t)l.tiles_n * l.tiles_k, pairs = kSms / 2, left = tiles % pairs, all = left * l.slices;
+  int64_t workers = left, best = (int64_t)l.slices * l.planes;
+  for (int64_t w = left + 1; left > 0 && w <= pairs && w <= all; ++w) {
+    const int64_t per = (all + w - 1) / w, cost = per * l.planes + (l.slices + per - 1) / per * 4 + kCost;
+    if (cost < best) {
       best = cost;
-      l.splits = (int)s;
+      workers = w;
     }
   }
+  const bool deal = workers > left;
+  l.left = (uint32_t)(deal ? left : 0);
+  l.whole = (uint32_t)(tiles - l.left);
+  l.workers = (uint32_t)(deal ? workers : 0);
   l.x = 0;
   l.dy = up(rows * l.x_pitch * 2, 256);
   l.parts = l.dy + (l.copy_dy ? up(rows * l.planes * l.dy_pitch * 2, 256) : 0);
-  l.bytes = l.parts + (l.splits > 1 ? up((int64_t)l.splits * n * k * 4, 256) : 0);
+  l.ready = l.parts + (deal ? (workers + left - 1) * kPart * 4 : 0);
+  l.bytes = l.ready + l.left * 64;
   return l;
 }
 
-template <bool OUT_BF16>
-cudaError_t launch_reduce(const float* parts, const WgradArgs& a, int splits, int sms, cudaStream_t s) {
-  const int64_t blocks = (a.n * a.k + 255) / 256, cap = (int64_t)sms * 16;
-  return launch_dependent(wgrad_reduce_kernel<OUT_BF16>, dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(256), 0, s,
-                          parts, a.grad, a.gs, a.n, a.k, splits, a.accumulate);
-}
-
-template <bool OUT_BF16>
-cudaError_t launch_product(const CUtensorMap& md, const CUtensorMap& mx, const ProductArgs& p, int sms, cudaStream_t s) {
+template <bool OUT_BF16, int PLANES>
+cudaError_t launch_product(const CUtensorMap& md, const CUtensorMap& mx, const ProductArgs& p, cudaStream_t s) {
   static PerDeviceOnce once;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   e = (cudaError_t)once.run(dev, [&] {
-    return (int)cudaFuncSetAttribute(wgrad_product_kernel<OUT_BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return (int)cudaFuncSetAttribute(wgrad_product_kernel<OUT_BF16, PLANES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)kSmem);
   });
   if (e != cudaSuccess) return e;
-  const uint32_t units = p.tiles_n * p.tiles_k * p.splits;
-  const uint32_t pairs = units < (uint32_t)(sms / 2) ? units : (uint32_t)(sms / 2);
+  uint32_t pairs = p.whole > p.workers ? p.whole : p.workers;
+  if (pairs > kSms / 2) pairs = kSms / 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs);
   cfg.blockDim = dim3(kThreads);
@@ -405,7 +602,7 @@ cudaError_t launch_product(const CUtensorMap& md, const CUtensorMap& mx, const P
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, wgrad_product_kernel<OUT_BF16>, md, mx, p);
+  return cudaLaunchKernelEx(&cfg, wgrad_product_kernel<OUT_BF16, PLANES>, md, mx, p);
 }
 
 }  // namespace
@@ -418,10 +615,13 @@ cudaError_t launch_wgrad(const WgradArgs& a, int dy_bf16, int grad_bf16, int sms
                          cudaStream_t s) {
   const int aligned = (uintptr_t)a.dy % 16 == 0 && a.dys % 8 == 0;
   const Layout l = layout_of(a.rows, a.n, a.k, dy_bf16, aligned);
-  const float* parts = reinterpret_cast<const float*>(ws + l.parts);
   if (a.rows == 0) {
     ++*launches;
-    return grad_bf16 ? launch_reduce<true>(parts, a, 0, sms, s) : launch_reduce<false>(parts, a, 0, sms, s);
+    const int64_t blocks = (a.n * a.k + 255) / 256, cap = (int64_t)sms * 16;
+    const unsigned g = (unsigned)(blocks < cap ? blocks : cap);
+    if (grad_bf16) wgrad_zero_kernel<true><<<g, 256, 0, s>>>(a.grad, a.gs, a.n, a.k);
+    else wgrad_zero_kernel<false><<<g, 256, 0, s>>>(a.grad, a.gs, a.n, a.k);
+    return cudaGetLastError();
   }
   MxArgs m = {};
   m.out = ws + l.x;
@@ -432,6 +632,8 @@ cudaError_t launch_wgrad(const WgradArgs& a, int dy_bf16, int grad_bf16, int sms
   m.xs = l.x_pitch;
   m.qs = a.qs;
   m.scs = a.scs;
+  m.zero = reinterpret_cast<uint32_t*>(ws + l.ready);
+  m.zeros = (int)l.left * 16;
   cudaError_t e = launch_mx_restore(m, 1, s);
   if (e != cudaSuccess) return e;
   ++*launches;
@@ -451,26 +653,29 @@ cudaError_t launch_wgrad(const WgradArgs& a, int dy_bf16, int grad_bf16, int sms
   if (e == cudaSuccess) e = operand_map(&mx, ws + l.x, a.rows, a.k, l.x_pitch);
   if (e != cudaSuccess) return e;
   ProductArgs p = {};
-  p.grad = l.splits > 1 ? (void*)parts : a.grad;
-  p.gs = l.splits > 1 ? a.k : a.gs;
+  p.grad = a.grad;
+  p.gs = a.gs;
+  p.parts = reinterpret_cast<float*>(ws + l.parts);
+  p.ready = reinterpret_cast<uint32_t*>(ws + l.ready);
   p.n = (uint32_t)a.n;
   p.k = (uint32_t)a.k;
-  p.tiles_n = (uint32_t)((a.n + kTile - 1) / kTile);
-  p.tiles_k = (uint32_t)((a.k + kTile - 1) / kTile);
-  p.splits = (uint32_t)l.splits;
-  p.slices = (uint32_t)((a.rows + kSlice - 1) / kSlice);
-  p.planes = (uint32_t)l.planes;
+  p.tiles_n = l.tiles_n;
+  p.tiles_k = l.tiles_k;
+  p.whole = l.whole;
+  p.left = l.left;
+  p.workers = l.workers;
+  p.share = l.workers ? l.left * l.slices / l.workers : 0;
+  p.extra = l.workers ? l.left * l.slices % l.workers : 0;
+  p.slices = l.slices;
   p.plane_rows = (uint32_t)a.rows;
   p.accumulate = a.accumulate;
+  p.vec = (uintptr_t)a.grad % 16 == 0 && a.gs % 4 == 0;
   p.status = a.status;
   p.wait_ns = a.wait_ns;
-  e = grad_bf16 ? launch_product<true>(md, mx, p, sms, s) : launch_product<false>(md, mx, p, sms, s);
+  if (l.planes == 1) e = grad_bf16 ? launch_product<true, 1>(md, mx, p, s) : launch_product<false, 1>(md, mx, p, s);
+  else e = grad_bf16 ? launch_product<true, 3>(md, mx, p, s) : launch_product<false, 3>(md, mx, p, s);
   if (e != cudaSuccess) return e;
   ++*launches;
-  if (l.splits > 1) {
-    e = grad_bf16 ? launch_reduce<true>(parts, a, l.splits, sms, s) : launch_reduce<false>(parts, a, l.splits, sms, s);
-    ++*launches;
-  }
   return e;
 }
 
