@@ -8,11 +8,12 @@
 //           neighbour one another in most vocabularies, so fall to different blocks) and reads all
 //           tokens: it counts those of lower residues (where its part of the sorted list begins)
 //           and places its own, stably, by per-warp counts of each id. No block waits for another.
-//   sums    a warp adds the rows of one run of equal ids (of one piece of a long run) over 256
-//           columns in fp32, all its loads independent, and writes that part of the gradient;
-//           pieces go to a workspace, and the warp that finishes a run's last piece adds them in
-//           their order. Between these blocks lie others that zero the rows of absent ids: most
-//           of the bytes where the vocabulary is large.
+//   sums    a warp adds, over 256 columns in fp32, the rows of the runs of equal ids (and of the
+//           pieces of long runs) that begin in a window of the sorted list, kAhead rows on the way
+//           at a time, and writes those parts of the gradient. Pieces' sums go to a workspace, and
+//           the warp that finishes the last of eight adds them in their order, eight such sums
+//           become one again, up to the run's. Between these blocks lie others that zero the rows
+//           of absent ids: most of the bytes where the vocabulary is large.
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -30,9 +31,11 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortIds = 1024;      // most ids of one block
 constexpr int kBatch = 16;          // tokens per lane that a sort warp loads at a time
-constexpr int kWindow = 8;          // sorted places per block of the sums
-constexpr int kPiece = 16;          // rows per piece of a long run (the last piece: up to 31)
-constexpr int kLong = 32;           // runs from this length on are summed in pieces
+constexpr int kWindow = 8;          // sorted places per warp of the sums
+constexpr int kFan = 8;             // sums that become one
+constexpr int kPiece = 8;           // rows per piece of a long run (the last piece: up to 15)
+constexpr int kLong = 16;           // runs from this length on are summed in pieces
+static_assert(kWindow <= kPiece, "a long piece ends past its window");
 constexpr int kCols = 256;          // columns per warp
 constexpr int kFillRows = 32;       // ids per zero-filling block
 
@@ -110,6 +113,9 @@ __global__ void __launch_bounds__(kSortThreads, 1) token_sort_kernel(EmbedGradAr
   };
   // lanes of one id among the lanes that have one (match only where there are several)
   auto peers = [&](int k, uint32_t in) { return (in & (in - 1)) == 0 ? in : __match_any_sync(0xffffffffu, k); };
+  const int64_t counts = (a.n + kPiece - 1) / kPiece * slices;
+  for (int64_t i = (int64_t)blockIdx.x * kSortThreads + threadIdx.x; i < counts; i += (int64_t)gridDim.x * kSortThreads)
+    a.count[i] = 0;
   for (int i = threadIdx.x; i < (kSortWarps * ids * (int)sizeof(Cnt) + 3) / 4; i += kSortThreads) smem[i] = 0;
   if (t0 < t1) read(t0, true);
   __syncthreads();
@@ -156,8 +162,6 @@ __global__ void __launch_bounds__(kSortThreads, 1) token_sort_kernel(EmbedGradAr
     base[b] = begin;
     length[b] = total;
     if (id < a.vocab) a.total[id] = total;
-    if (total >= kLong)
-      for (int i = 0; i < slices; ++i) a.count[(int64_t)(begin / kPiece) * slices + i] = 0;
   }
   if (me == mask && b == kSortThreads - 1) a.total[a.vocab] = begin + total;   // the last residue's end
   __syncthreads();
@@ -216,11 +220,61 @@ __device__ __forceinline__ void write_grad(const EmbedGradArgs& a, int64_t id, c
   }
 }
 
-// `sums` blocks for kWindow sorted places each, spread evenly among the blocks that write zeros
-// (none when accumulating): the sums wait on memory latency while the zeros fill its bandwidth.
+// The sum of piece k of np of a run whose pieces' slots begin at `first` meets the others': true for
+// the warp that has the run's sum in the end. Level by level, the last to finish of (up to) kFan
+// neighbours adds them in order, into the first one's slot. Counters: of a group of several, the
+// slot of its first member plus the level, which lies within the group.
+template <int V>
+__device__ __forceinline__ bool join_pieces(const EmbedGradArgs& a, const Cols<V>& w, int64_t first, int k, int np, int slice,
+                                            int slices, int lane, float (&sum)[Cols<V>::N][V]) {
+  constexpr int N = Cols<V>::N, kAtOnce = V == 8 ? 4 : 2;
+  int64_t stride = 1;
+  for (int level = 0; np > 1; ++level) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (w.ok(j)) store_v<V, false>(a.partial, (first + k * stride) * a.dim + w.at(j), sum[j]);
+    const int group = k / kFan, members = min(kFan, np - group * kFan);
+    if (members > 1) {
+      __threadfence();
+      __syncwarp();
+      int done = 0;
+      if (lane == 0) done = atomicAdd(a.count + (first + group * kFan * stride + level) * slices + slice, 1);
+      if (__shfl_sync(0xffffffffu, done, 0) != members - 1) return false;
+      __threadfence();
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+#pragma unroll
+        for (int e = 0; e < V; ++e) sum[j][e] = 0.0f;
+      for (int m = 0; m < members; m += kAtOnce) {
+        float v[kAtOnce][N][V];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            if (m + u < members && w.ok(j)) load_cg<V>(a.partial + (first + (group * kFan + m + u) * stride) * a.dim + w.at(j), v[u][j]);
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            if (m + u < members && w.ok(j)) {
+#pragma unroll
+              for (int e = 0; e < V; ++e) sum[j][e] += v[u][j][e];
+            }
+      }
+    }
+    k = group;
+    np = (np + kFan - 1) / kFan;
+    stride *= kFan;
+  }
+  return true;
+}
+
+// `sums` blocks of eight warps, a window and a slice of the columns each, spread evenly among the
+// blocks that write zeros (none when accumulating): the sums wait on memory latency while the zeros
+// fill its bandwidth.
 template <int V, bool D_BF16, bool G_BF16>
-__global__ void __launch_bounds__(kThreads, V == 8 ? (D_BF16 ? 4 : 3) : 2) embed_sum_kernel(EmbedGradArgs a, int64_t sums, int64_t fills, int slices) {
-  constexpr int N = Cols<V>::N;
+__global__ void __launch_bounds__(kThreads, V == 8 ? 3 : 2) embed_sum_kernel(EmbedGradArgs a, int64_t sums, int64_t fills, int slices) {
+  constexpr int N = Cols<V>::N, kAhead = V == 8 ? 4 : 2;
   grid_dependency_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t blk = blockIdx.x, all = sums + fills;
@@ -241,115 +295,87 @@ __global__ void __launch_bounds__(kThreads, V == 8 ? (D_BF16 ? 4 : 3) : 2) embed
     return;
   }
   // the places of the window and of the rows that its pieces may reach past it
-  const int64_t p0 = before * kWindow;
+  const int64_t item = before * (kThreads / 32) + warp, p0 = item / slices * kWindow;
+  const int slice = (int)(item % slices);
+  static_assert(kWindow + kLong - 1 <= 32, "a lane per place");
   int4 me = make_int4(0, 0, 0, 0);
-  int far = 0;
   if (p0 + lane < a.n) me = a.sorted[p0 + lane];
-  if (lane < kWindow && p0 + 32 + lane < a.n) far = a.sorted[p0 + 32 + lane].y;
   const int64_t valid = a.total[a.vocab];
-  if (p0 >= valid) return;
   // the pieces that begin in this window: whole runs shorter than kLong, else every kPiece rows
-  // (the last piece takes the rest, so that pieces of long runs are at least kPiece apart)
+  // (the last piece takes the rest, so that pieces of long runs are at least kPiece apart). One
+  // follows the other, so their rows are the places from the first one's on.
   const int pieces = me.w < kLong ? 1 : me.w / kPiece;
   const bool head = lane < kWindow && p0 + lane < valid &&
                     (me.w < kLong ? me.z == 0 : me.z % kPiece == 0 && me.z / kPiece < pieces);
   const uint32_t heads = __ballot_sync(0xffffffffu, head);
-  const int rank = __popc(heads & ((1u << lane) - 1u));
-  const int items = __popc(heads) * slices;
-  for (int it = warp; it < items; it += kThreads / 32) {
-    const int slice = it % slices;
-    const int src = __ffs(__ballot_sync(0xffffffffu, head && rank == it / slices)) - 1;
-    const int id = __shfl_sync(0xffffffffu, me.x, src), off = __shfl_sync(0xffffffffu, me.z, src);
-    const int len = __shfl_sync(0xffffffffu, me.w, src), np = __shfl_sync(0xffffffffu, pieces, src);
-    const int64_t p = p0 + src;
-    const bool whole = np == 1;
-    const int n = whole ? len : (off / kPiece == np - 1 ? len - off : kPiece);   // at most 31 rows
-    const int near_pos = __shfl_sync(0xffffffffu, me.y, (src + lane) & 31);
-    const int far_pos = __shfl_sync(0xffffffffu, far, (src + lane) & 31);
-    const int pos = src + lane < 32 ? near_pos : far_pos;   // row of the piece's lane-th place
-    const Cols<V> w = {(int64_t)slice * kCols + lane * V, a.dim};
-    Raw<V, G_BF16> old[N];
-    if (a.accumulate && whole) {
+  if (!heads) return;
+  const int rows = pieces == 1 ? me.w : (me.z / kPiece == pieces - 1 ? me.w - me.z : kPiece);   // at most 15
+  const uint32_t ends = __reduce_or_sync(0xffffffffu, head ? 1u << (lane + rows - 1) : 0u);
+  const int stop = 32 - __clz(ends);
+  const Cols<V> w = {(int64_t)slice * kCols + lane * V, a.dim};
+  float sum[N][V];
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int e = 0; e < V; ++e) sum[j][e] = 0.0f;
+  for (int i0 = __ffs(heads) - 1; i0 < stop; i0 += kAhead) {
+    Raw<V, D_BF16> v[kAhead][N];
+    Raw<V, G_BF16> old[kAhead][N];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + u;
+      if (i >= stop) break;
+      const int64_t row = (int64_t)__shfl_sync(0xffffffffu, me.y, i) * a.dy_stride;
 #pragma unroll
       for (int j = 0; j < N; ++j)
-        if (w.ok(j)) old[j].load(a.grad, id * a.grad_stride + w.at(j));
-    }
-    float sum[N][V];
+        if (w.ok(j)) v[u][j].load(a.dy, row + w.at(j));
+      if (a.accumulate && (ends >> i & 1)) {
+        const int src = 31 - __clz(heads & (2u << min(i, kWindow - 1)) - 1u);
+        const int id = __shfl_sync(0xffffffffu, me.x, src), np = __shfl_sync(0xffffffffu, pieces, src);
+        if (np == 1) {
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-#pragma unroll
-      for (int e = 0; e < V; ++e) sum[j][e] = 0.0f;
-    constexpr int kAhead = 4;
-    for (int i0 = 0; i0 < n; i0 += kAhead) {
-      Raw<V, D_BF16> v[kAhead][N];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (i0 + u >= n) break;
-        const int64_t row = (int64_t)__shfl_sync(0xffffffffu, pos, i0 + u) * a.dy_stride;
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-          if (w.ok(j)) v[u][j].load(a.dy, row + w.at(j));
-      }
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (i0 + u >= n) break;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          if (!w.ok(j)) continue;
-          float f[V];
-          v[u][j].get(f);
-#pragma unroll
-          for (int e = 0; e < V; ++e) sum[j][e] += f[e];
+          for (int j = 0; j < N; ++j)
+            if (w.ok(j)) old[u][j].load(a.grad, id * a.grad_stride + w.at(j));
         }
       }
     }
-    if (whole) {
-      write_grad<V, G_BF16>(a, id, w, old, sum);
-      continue;
-    }
-    // slot p / kPiece: no other piece of a long run has it. The run's slots follow one another.
-    const int64_t first = (p - off) / kPiece;
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (w.ok(j)) store_v<V, false>(a.partial, (p / kPiece) * a.dim + w.at(j), sum[j]);
-    __threadfence();
-    __syncwarp();
-    int done = 0;
-    if (lane == 0) done = atomicAdd(a.count + first * slices + slice, 1);
-    if (__shfl_sync(0xffffffffu, done, 0) != np - 1) continue;
-    __threadfence();
-    if (a.accumulate) {
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + u;
+      if (i >= stop) break;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        if (!w.ok(j)) continue;
+        float f[V];
+        v[u][j].get(f);
+#pragma unroll
+        for (int e = 0; e < V; ++e) sum[j][e] += f[e];
+      }
+      if (!(ends >> i & 1)) continue;
+      const int src = 31 - __clz(heads & (2u << min(i, kWindow - 1)) - 1u);
+      const int id = __shfl_sync(0xffffffffu, me.x, src), np = __shfl_sync(0xffffffffu, pieces, src);
+      if (np > 1) break;   // a long run's piece, which reaches past the window: the last one
+      write_grad<V, G_BF16>(a, id, w, old[u], sum);
 #pragma unroll
       for (int j = 0; j < N; ++j)
-        if (w.ok(j)) old[j].load(a.grad, id * a.grad_stride + w.at(j));
+#pragma unroll
+        for (int e = 0; e < V; ++e) sum[j][e] = 0.0f;
     }
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-#pragma unroll
-      for (int e = 0; e < V; ++e) sum[j][e] = 0.0f;
-    constexpr int kParts = 2;
-    for (int k0 = 0; k0 < np; k0 += kParts) {
-      float v[kParts][N][V];
-#pragma unroll
-      for (int u = 0; u < kParts; ++u) {
-        if (k0 + u >= np) break;
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-          if (w.ok(j)) load_cg<V>(a.partial + (first + k0 + u) * a.dim + w.at(j), v[u][j]);
-      }
-#pragma unroll
-      for (int u = 0; u < kParts; ++u) {
-        if (k0 + u >= np) break;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          if (!w.ok(j)) continue;
-#pragma unroll
-          for (int e = 0; e < V; ++e) sum[j][e] += v[u][j][e];
-        }
-      }
-    }
-    write_grad<V, G_BF16>(a, id, w, old, sum);
   }
+  const uint32_t longs = __ballot_sync(0xffffffffu, head && pieces > 1);
+  if (!longs) return;
+  const int src = __ffs(longs) - 1;
+  const int id = __shfl_sync(0xffffffffu, me.x, src), off = __shfl_sync(0xffffffffu, me.z, src);
+  const int np = __shfl_sync(0xffffffffu, pieces, src);
+  // slot p / kPiece: no other piece of a long run has it. The run's slots follow one another.
+  if (!join_pieces<V>(a, w, (p0 + src - off) / kPiece, off / kPiece, np, slice, slices, lane, sum)) return;
+  Raw<V, G_BF16> old[N];
+  if (a.accumulate) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (w.ok(j)) old[j].load(a.grad, id * a.grad_stride + w.at(j));
+  }
+  write_grad<V, G_BF16>(a, id, w, old, sum);
 }
 
 bool aligned8(const void* p, int64_t stride) { return (uintptr_t)p % 16 == 0 && stride % 8 == 0; }
@@ -375,7 +401,7 @@ int slices_of(int64_t dim) { return (int)((dim + kCols - 1) / kCols); }
 
 template <int V, bool D, bool G>
 cudaError_t embed_sums(const EmbedGradArgs& a, int64_t* launches, cudaStream_t s) {
-  const int64_t sums = (a.n + kWindow - 1) / kWindow;
+  const int64_t sums = ((a.n + kWindow - 1) / kWindow * slices_of(a.dim) + kThreads / 32 - 1) / (kThreads / 32);
   const int64_t fills = a.accumulate ? 0 : (a.vocab + kFillRows - 1) / kFillRows;
   ++*launches;
   return launch_dependent(embed_sum_kernel<V, D, G>, dim3((unsigned)(sums + fills)), dim3(kThreads), 0, s, a, sums, fills,

@@ -31,8 +31,8 @@ struct EmbedGradArgs {
   // workspace
   int4* sorted;    // [n] tokens grouped by id: id, position, place in the run of the id, length of the run
   int* total;      // [vocab + 1] tokens of each id; total[vocab] = tokens in all
-  float* partial;  // [ceil(n / 16)][dim] sums of the pieces of long runs
-  int* count;      // [ceil(n / 16)][slices] finished pieces of each long run
+  float* partial;  // [ceil(n / 8)][dim] sums of the pieces of long runs
+  int* count;      // [ceil(n / 8)][slices] finished sums of each group of pieces
 };
 int64_t embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim, EmbedGradArgs* a, char* base);
 cudaError_t launch_embedding_grad(const EmbedGradArgs& a, int dy_bf16, int grad_bf16, int id64,
