@@ -1,4 +1,5 @@
-"""Builds libmuon.so (the sm_100a kernels and the C ABI) in-tree with nvcc."""
+"""Builds, in-tree, libmuon.so (the sm_100a kernels and the C ABI) with nvcc, and _plain.so (the plain
+case of the gradient operators' Python calls, csrc/binding.cpp) with g++."""
 from __future__ import annotations
 
 import os
@@ -49,6 +50,39 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     return LIB
 
 
+BINDING = os.path.join(HERE, "_plain.so")
+
+
+def binding_stale() -> bool:
+    if not os.path.exists(BINDING):
+        return True
+    t = os.path.getmtime(BINDING)
+    return any(os.path.getmtime(d) > t for d in (os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "muon.h")))
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    if not force and not binding_stale():
+        return BINDING
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    inc, libs = os.path.join(home, "include"), os.path.join(home, "lib")
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    out = f"{BINDING}.{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-Wno-attributes",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "binding.cpp"), "-o", out,
+           "-L", libs, "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", f"-Wl,-rpath,{libs}"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.check_call(cmd)
+    os.replace(out, BINDING)
+    return BINDING
+
+
 if __name__ == "__main__":
     build(force="--force" in sys.argv, verbose=True,
           extra=["-Xptxas", "-v"] if "--ptxas" in sys.argv else [])
+    build_binding(force="--force" in sys.argv, verbose=True)

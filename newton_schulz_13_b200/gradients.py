@@ -7,7 +7,10 @@ the root-mean-square norm, and 8-bit activation checkpoints with the weight grad
     dx, dw = ns.rms_norm_grad(dy, h, w, rstd, dh=dh)              # adamw_step's gradient of a norm scale
     dE = ns.embedding_grad(tokens, dx, vocab, scale=s)            # adamw_step's gradient of the table
 
-Argument marshalling only, as in the rest of the package; include/muon.h has the formulas. Inputs
+Argument marshalling only, as in the rest of the package; include/muon.h has the formulas. The plain
+case of a call (contiguous tensors of the current device, outputs to be allocated, the current
+stream) goes through _plain.so (csrc/binding.cpp): 4-7 us of the interpreter's time instead of 10-23.
+Any other, and any that is refused, takes the path below through ctypes. Inputs
 are CUDA tensors whose last dimension is contiguous (rows may be strided); leading dimensions are
 taken as rows. Outputs and workspaces come from torch's allocator on the stream the call runs on
 (`stream`, or the current stream of the tensors' device), so calls on several streams, and calls
@@ -17,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import warnings
 from typing import NamedTuple, Optional
 
 import torch
@@ -41,6 +45,27 @@ for _name, _args in {"muon_embedding_grad_workspace": [_i64, _i64, _i64], "muon_
                      "muon_weight_grad_workspace": [_i64, _i64, _i64, _int]}.items():
     getattr(lib, _name).argtypes = _args
     getattr(lib, _name).restype = _i64
+
+
+
+def _load_plain():
+    """The extension, built if it is missing or older than its source; None where that fails: every
+    call then takes the path through ctypes, to the same kernels."""
+    from . import build as _build
+    try:
+        if _build.binding_stale():
+            _build.build_binding()
+        from . import _plain
+    except Exception as e:  # noqa: BLE001
+        warnings.warn(f"{_build.BINDING} is not usable ({e}); calls go through ctypes")
+        return None
+    _plain.bind(*(ctypes.cast(getattr(lib, "muon_" + n), _vp).value for n in (
+        "embedding", "embedding_grad", "embedding_grad_workspace", "rms_norm", "rms_norm_grad", "rms_norm_grad_workspace",
+        "checkpoint_store", "checkpoint_restore", "weight_grad", "weight_grad_workspace")))
+    return _plain
+
+
+_fast = _load_plain()
 
 _CODE = {torch.bfloat16: BF16, torch.float32: FP32}
 _Q, _S = torch.float8_e4m3fn, torch.float8_e8m0fnu
@@ -158,6 +183,10 @@ def embedding(tokens, table, scale: float = 1.0, out=None, out_dtype=None, strea
     """out[..., :] = scale * table[tokens]; tokens int32 or int64 of any shape, table [vocab, dim]
     bf16 or fp32, out in out_dtype (default: the table's). A negative id gives a row of zeros, and
     so does an id past the vocabulary, which check_status() then reports (WARN_TOKEN)."""
+    if out is None and stream is None and _fast is not None:
+        out = _fast.embedding(tokens, table, scale, out_dtype)
+        if out is not None:
+            return out
     dev = _device(tokens, "tokens")
     bits = _tokens(tokens)
     ts = _rows(table, "table", dev)
@@ -186,6 +215,10 @@ def embedding_grad(tokens, dy, vocab: int, scale: float = 1.0, grad=None, grad_d
     [vocab, dim] in grad_dtype (default: dy's), zeros for absent tokens. With accumulate, added to
     `grad`, of which only the rows of present tokens are touched. The sums are fp32, in the order of
     the tokens; negative and too large ids contribute nothing."""
+    if stream is None and _fast is not None:
+        got = _fast.embedding_grad(tokens, dy, vocab, scale, grad, grad_dtype, accumulate)
+        if got is not None:
+            return got if grad is None else grad
     dev = _device(tokens, "tokens")
     bits = _tokens(tokens)
     ds = _rows(dy, "dy", dev)
@@ -246,6 +279,11 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-5, output: bool = True, c
     x's type, rstd = 1 / rms(h) per row (fp32), and with checkpoint=True an ActCheckpoint of y.
     output=False leaves y out (y None). `h` and `y` may be given as buffers: h may be the residual
     or, in its type, x; y may be x."""
+    if h is None and y is None and stream is None and _fast is not None:
+        got = _fast.rms_norm(x, weight, residual, eps, output, checkpoint)
+        if got is not None:
+            y, h, rstd, q, s = got
+            return RmsNorm(y, x if h is None else h, rstd, None if q is None else ActCheckpoint(q, s))
     dev = _device(x, "x")
     xs = _rows(x, "x", dev)
     shape = x.shape
@@ -299,6 +337,10 @@ def rms_norm_grad(dy, h, weight, rstd, dh=None, dx=None, dweight=None, accumulat
     returned: (dx, dweight), dx in h's type and dweight fp32. dh, in h's type, is the gradient that
     reaches h from elsewhere and is added to dx. With accumulate, dweight is added to the given
     `dweight`. dx may be one of dy, h and dh where the types agree."""
+    if dx is None and dweight is None and not accumulate and stream is None and _fast is not None:
+        got = _fast.rms_norm_grad(dy, h, weight, rstd, dh)
+        if got is not None:
+            return got
     dev = _device(h, "h")
     hs = _rows(h, "h", dev)
     shape = h.shape
@@ -347,6 +389,10 @@ def checkpoint_store(x, out: Optional[ActCheckpoint] = None, stream=None) -> Act
     """x [..., dim] (bf16 or fp32) in 8 bits: e4m3 values in blocks of 32 along a row, each under the
     smallest power of two that keeps its largest value within e4m3's range. A block with an
     infinity or a NaN becomes NaN."""
+    if out is None and stream is None and _fast is not None:
+        got = _fast.checkpoint_store(x)
+        if got is not None:
+            return ActCheckpoint(*got)
     dev = _device(x, "x")
     xs = _rows(x, "x", dev)
     dim = x.shape[-1]
@@ -368,6 +414,10 @@ def checkpoint_store(x, out: Optional[ActCheckpoint] = None, stream=None) -> Act
 
 def checkpoint_restore(checkpoint: ActCheckpoint, dtype=torch.bfloat16, out=None, stream=None):
     """The values of a checkpoint, in bf16 (exact for what checkpoint_store and rms_norm make) or fp32."""
+    if out is None and stream is None and _fast is not None and type(checkpoint) is ActCheckpoint:
+        x = _fast.checkpoint_restore(checkpoint[0], checkpoint[1], dtype)
+        if x is not None:
+            return x
     dev, qs, ss = _checkpoint(checkpoint, "checkpoint")
     q, s = checkpoint
     dim = xs = q.shape[-1]
@@ -389,6 +439,10 @@ def weight_grad(dy, checkpoint: ActCheckpoint, grad=None, grad_dtype=None, accum
     """Gradient of y = x @ W.T by W, from dy [..., n] (bf16 or fp32) and the checkpoint of x [..., k]:
     grad[n, k] = sum over the rows of dy^T x, in grad_dtype (default: dy's), summed in fp32. With
     accumulate, added to `grad`. It is what muon_step takes as a gradient."""
+    if stream is None and _fast is not None and type(checkpoint) is ActCheckpoint:
+        got = _fast.weight_grad(dy, checkpoint[0], checkpoint[1], grad, grad_dtype, accumulate)
+        if got is not None:
+            return got if grad is None else grad
     dev, qs, ss = _checkpoint(checkpoint, "checkpoint")
     q, s = checkpoint
     ds = _rows(dy, "dy", dev)

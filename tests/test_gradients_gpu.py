@@ -695,6 +695,41 @@ def test_graphs_and_streams():
     assert ns.check_status() == ns.OK
 
 
+def test_plain_calls_and_full_path_agree(monkeypatch):
+    """Calls that take the extension's path give what the path through ctypes gives."""
+    import newton_schulz_13_b200 as ns
+    ns.ActCheckpoint
+    from newton_schulz_13_b200 import gradients
+    assert gradients._fast is not None
+    x, r, w = normal((3, 50, 72), BF16, 120), normal((3, 50, 72), FP32, 121), normal((72,), FP32, 122)
+    t = tokens_of(150, 40, 123, torch.int32).view(3, 50)
+    table, dy = normal((40, 72), FP32, 124), normal((3, 50, 24), FP32, 125)
+    ck = ns.checkpoint_store(x)
+    buf_e, buf_w = normal((40, 72), FP32, 126), normal((24, 72), FP32, 127)
+    f = ns.rms_norm(x, w, residual=r)
+    calls = [
+        lambda: [ns.embedding(t, table), ns.embedding(t, table, scale=2, out_dtype=BF16)],
+        lambda: [ns.embedding_grad(t, x, 40), ns.embedding_grad(t, x, 40, scale=0.5, grad_dtype=FP32),
+                 ns.embedding_grad(t, x, 40, grad=buf_e.clone(), accumulate=True), ns.embedding_grad(t, x, 40, grad=buf_e.clone())],
+        lambda: [*ns.rms_norm(x, w)[:3], *ns.rms_norm(x, w, residual=r, eps=0.1)[:3]],
+        lambda: [*ns.rms_norm(x, w, residual=r, checkpoint=True, output=False).checkpoint, *ns.rms_norm(r, w.to(BF16), checkpoint=True).checkpoint],
+        lambda: [*ns.rms_norm_grad(x, f.h, w, f.rstd), *ns.rms_norm_grad(x, f.h, w, f.rstd, dh=r)],
+        lambda: [*ns.checkpoint_store(x), *ns.checkpoint_store(r), ns.checkpoint_restore(ck), ns.checkpoint_restore(ck, dtype=FP32)],
+        lambda: [ns.weight_grad(dy, ck), ns.weight_grad(dy.to(BF16), ck, grad_dtype=FP32),
+                 ns.weight_grad(dy, ck, grad=buf_w.clone(), accumulate=True)],
+        lambda: [ns.embedding(t[0, 0], table), ns.embedding(t[:0], table), *ns.checkpoint_store(x[:0]), *ns.rms_norm(x[:0], w)[:3]],
+    ]
+    for i, call in enumerate(calls):
+        fast = call()
+        with monkeypatch.context() as m:
+            m.setattr(gradients, "_fast", None)
+            full = call()
+        for k, (a, b) in enumerate(zip(fast, full)):
+            assert a.dtype == b.dtype and a.shape == b.shape and a.stride() == b.stride(), (i, k)
+            assert torch.equal(a.contiguous().view(torch.uint8) if a.dim() else a, b.contiguous().view(torch.uint8) if b.dim() else b), (i, k)
+    assert ns.check_status() == ns.OK
+
+
 def test_refusals_of_layouts_and_types():
     import newton_schulz_13_b200 as ns
     x = normal((6, 64), BF16, 110)
