@@ -13,7 +13,7 @@ LIB = os.path.join(HERE, "libmuon.so")
 SOURCES = ["api.cu", "elementwise.cu", "ns_gemm.cu", "ns_gemm_x3.cu", "noalloc.cu",
            "ops_api.cu", "embedding.cu", "rmsnorm.cu", "checkpoint.cu", "weight_grad.cu"]
 HEADERS = ["muon_internal.h", "ptx.cuh", "tile_sched.cuh", "device_once.h", "pair_pipe.cuh",
-           "ops_internal.h", "vec_io.cuh", "mx.cuh"]
+           "ops_internal.h", "vec_io.cuh", "mx.cuh", "fast_div.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

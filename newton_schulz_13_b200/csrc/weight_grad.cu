@@ -23,6 +23,7 @@
 #include <stdint.h>
 
 #include "device_once.h"
+#include "fast_div.cuh"
 #include "muon_internal.h"
 #include "mx.cuh"
 #include "ops_internal.h"
@@ -483,28 +484,49 @@ __global__ void __launch_bounds__(256) wgrad_zero_kernel(void* grad, int64_t gs,
     store1<OUT_BF16>(grad, t / k * gs + t % k, 0.0f);
 }
 
-// Copies dy into bf16 rows of `pitch` elements; an fp32 dy into three planes, plane_rows apart.
-template <bool DY_BF16>
-__global__ void __launch_bounds__(256) wgrad_stage_dy_kernel(const void* dy, int64_t dys, int64_t rows, int64_t n,
-                                                             __nv_bfloat16* out, int64_t pitch) {
-  const int64_t total = rows * n;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t t = i / n, c = i - t * n;
-    if constexpr (DY_BF16) {
-      out[t * pitch + c] = static_cast<const __nv_bfloat16*>(dy)[t * dys + c];
-    } else {
-      float v = static_cast<const float*>(dy)[t * dys + c];
+// Copies dy into bf16 rows of `pitch` elements; an fp32 dy into three planes, plane_rows apart. A
+// thread has V columns (8 where dy's rows are aligned); per_row: such groups of a row, total: of all
+// rows, below 2^31.
+template <bool DY_BF16, int V>
+__global__ void __launch_bounds__(256) wgrad_stage_dy_kernel(const void* dy, int64_t dys, int64_t plane_rows,
+                                                             __nv_bfloat16* out, int64_t pitch, Div per_row, uint32_t total) {
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= total) return;
+  const uint32_t t = per_row.quot(i), c = (i - t * per_row.d) * V;
+  float v[V];
+  load_v<V, DY_BF16>(dy, t * dys + c, v);
+  if constexpr (DY_BF16) {
+    store_v<V, true>(out, t * pitch + c, v);
+  } else {
 #pragma unroll
-      for (int p = 0; p < 3; ++p) {
+    for (int p = 0; p < 3; ++p) {
+      float part[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
         // the top 16 bits of a float are its value truncated to bf16; infinities and NaN stay whole
-        uint32_t top = __float_as_uint(v) & 0xffff0000u;
+        uint32_t top = __float_as_uint(v[e]) & 0xffff0000u;
         const bool finite = (top & 0x7f800000u) != 0x7f800000u;
-        if (!finite && (__float_as_uint(v) & 0x7fffffu)) top |= 0x00400000u;
-        out[(p * rows + t) * pitch + c] = __float2bfloat16_rn(__uint_as_float(top));
-        v = finite ? v - __uint_as_float(top) : 0.0f;
+        if (!finite && (__float_as_uint(v[e]) & 0x7fffffu)) top |= 0x00400000u;
+        part[e] = __uint_as_float(top);
+        v[e] = finite ? v[e] - part[e] : 0.0f;
       }
+      store_v<V, true>(out, (p * plane_rows + t) * pitch + c, part);
     }
   }
+}
+
+template <bool DY_BF16, int V>
+cudaError_t launch_stage_dy(const WgradArgs& a, __nv_bfloat16* out, int64_t pitch, cudaStream_t s) {
+  const int64_t per_row = a.n / V, most = ((int64_t(1) << 31) - 1) / per_row;
+  for (int64_t r = 0; r < a.rows; r += most) {
+    const int64_t total = (a.rows - r < most ? a.rows - r : most) * per_row;
+    const char* from = static_cast<const char*>(a.dy) + r * a.dys * (DY_BF16 ? 2 : 4);
+    wgrad_stage_dy_kernel<DY_BF16, V><<<(unsigned)((total + 255) / 256), 256, 0, s>>>(
+        from, a.dys, a.rows, out + r * pitch, pitch, Div((uint32_t)per_row), (uint32_t)total);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -638,12 +660,11 @@ cudaError_t launch_wgrad(const WgradArgs& a, int dy_bf16, int grad_bf16, int sms
   if (e != cudaSuccess) return e;
   ++*launches;
   if (l.copy_dy) {
-    const int64_t blocks = (a.rows * a.n + 255) / 256, cap = (int64_t)sms * 16;
-    const unsigned g = (unsigned)(blocks < cap ? blocks : cap);
     __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(ws + l.dy);
-    if (dy_bf16) wgrad_stage_dy_kernel<true><<<g, 256, 0, s>>>(a.dy, a.dys, a.rows, a.n, out, l.dy_pitch);
-    else wgrad_stage_dy_kernel<false><<<g, 256, 0, s>>>(a.dy, a.dys, a.rows, a.n, out, l.dy_pitch);
-    e = cudaGetLastError();
+    const bool v8 = a.n % 8 == 0 && (uintptr_t)a.dy % 16 == 0 && a.dys % 4 == 0;
+    if (dy_bf16) e = launch_stage_dy<true, 1>(a, out, l.dy_pitch, s);
+    else if (v8) e = launch_stage_dy<false, 8>(a, out, l.dy_pitch, s);
+    else e = launch_stage_dy<false, 1>(a, out, l.dy_pitch, s);
     if (e != cudaSuccess) return e;
     ++*launches;
   }
