@@ -1,6 +1,6 @@
 // The plain case of the gradient operators' Python calls without the interpreter's share of the
 // argument checks, allocations and ctypes conversions, which cost more than the launch of a small
-// call (one row through the norm: 16 us a call with them, see gradients.py for the figure without).
+// call (one row through the norm: 16 us a call with them, 7 without).
 //
 // Plain: exact torch tensors on the current device, contiguous, of supported and matching types and
 // shapes, outputs to be allocated, the current stream. Each function returns None for any other

@@ -116,8 +116,12 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(NormArgs a) {
       uint32_t m = 0;
 #pragma unroll
       for (int e = 0; e < V; ++e) m = max(m, __float_as_uint(y[e]) & 0x7fffffffu);
+      if constexpr (V == 1) {
+        m = __reduce_max_sync(0xffffffffu, m);
+      } else {
 #pragma unroll
-      for (int o = kMxBlock / V / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int o = kMxBlock / V / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      }
       if (ok) {
         const uint32_t code = mx_scale_code(m);
         uint8_t* q = a.q + row * a.qs + i * V;
@@ -275,11 +279,29 @@ struct GradSlot {
   static constexpr int kPitch = odd(kDh), kPitchDh = odd(2 * kDh - kH);
 };
 
-// Copies one element into its slot: asynchronously if fp32.
-template <bool BF16>
-__device__ __forceinline__ void stage_element(char* slot, const void* base, int64_t i) {
-  if constexpr (BF16) *reinterpret_cast<__nv_bfloat16*>(slot) = static_cast<const __nv_bfloat16*>(base)[i];
-  else cp_async<4>(slot, static_cast<const float*>(base) + i);
+// Copies a thread's `mine` elements of a tensor (base: its first, step apart) into its slot:
+// asynchronously if fp32, else through registers, all loads before the first store.
+template <int VPT, bool BF16>
+__device__ __forceinline__ void stage_elements(char* slot, const void* base, int64_t i, int step, int mine) {
+  if constexpr (BF16) {
+    __nv_bfloat16 v[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      if (j >= mine) break;
+      v[j] = static_cast<const __nv_bfloat16*>(base)[i + j * step];
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      if (j >= mine) break;
+      reinterpret_cast<__nv_bfloat16*>(slot)[j] = v[j];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      if (j >= mine) break;
+      cp_async<4>(slot + j * 4, static_cast<const float*>(base) + i + j * step);
+    }
+  }
 }
 
 // A row group takes every (gridDim.x * groups)-th row; each thread keeps the weight gradient of its
@@ -329,14 +351,9 @@ __global__ void __launch_bounds__(FEED == Feed::kDirect ? 1024 : 512) rms_norm_g
       if (a.dh) bulk_load(to + dh_at, static_cast<const char*>(a.dh) + row * a.dhs * kH, (uint32_t)a.dim * kH, bar);
     } else if constexpr (COPIES) {
       if (row < a.rows) {
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-          if (j >= mine) break;
-          const int64_t c = j * tpr + tid;
-          stage_element<DY_BF16>(to + at(j, kDy), a.dy, row * a.dys + c);
-          stage_element<H_BF16>(to + h_at + at(j, kH), a.h, row * a.hs + c);
-          if (a.dh) stage_element<H_BF16>(to + dh_at + at(j, kH), a.dh, row * a.dhs + c);
-        }
+        stage_elements<VPT, DY_BF16>(to, a.dy, row * a.dys + tid, tpr, mine);
+        stage_elements<VPT, H_BF16>(to + h_at, a.h, row * a.hs + tid, tpr, mine);
+        if (a.dh) stage_elements<VPT, H_BF16>(to + dh_at, a.dh, row * a.dhs + tid, tpr, mine);
       }
       cp_async_commit();
     }
