@@ -140,15 +140,35 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(NormArgs a) {
 constexpr int kMaxGroups = 16, kRingStages = 3, kGradStages = 4;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
-template <bool X_BF16, bool R_BF16>
+// A row of n bytes at p by bulk copy: the 16-byte granules that hold it, of which it begins at byte
+// p % 16 (0 where V = 8); `room` is the most that they take. Each granule holds a byte of the row, so
+// it lies in the row's allocation; what it holds of others is not used.
+template <int V>
+__host__ __device__ constexpr int row_room(int n) {
+  return V == 8 ? n : (n + 30) / 16 * 16;
+}
+template <int V>
+__device__ __forceinline__ uint32_t row_off(const void* base, int64_t bytes) {
+  return V == 8 ? 0u : (uint32_t)((uintptr_t)base + bytes) & 15u;
+}
+template <int V>
+__device__ __forceinline__ uint32_t row_span(const void* base, int64_t bytes, int n) {
+  return V == 8 ? (uint32_t)n : (row_off<V>(base, bytes) + n + 15u) & ~15u;
+}
+template <int V>
+__device__ __forceinline__ void row_load(void* to, const void* base, int64_t bytes, int n, uint64_t* bar) {
+  bulk_load(to, static_cast<const char*>(base) + bytes - row_off<V>(base, bytes), row_span<V>(base, bytes, n), bar);
+}
+
+template <int V, bool X_BF16, bool R_BF16>
 __global__ void __launch_bounds__(512, 1) rms_norm_ring_kernel(NormArgs a) {
   extern __shared__ __align__(128) char stages[];
-  constexpr int VPT = 2, S = kRingStages, kX = X_BF16 ? 2 : 4, kR = R_BF16 ? 2 : 4;
+  constexpr int VPT = V == 8 ? 2 : 16, S = kRingStages, kX = X_BF16 ? 2 : 4, kR = R_BF16 ? 2 : 4;
   __shared__ float red[2][32];
   __shared__ uint64_t full[kMaxGroups][S];
   __shared__ int abort_word[2];   // a wait gave up; never set (for the last waits)
   const int tid = threadIdx.x, tpr = blockDim.x, warps = tpr >> 5, group = threadIdx.y;
-  const int dim = (int)a.dim, nv = dim / 8;
+  const int dim = (int)a.dim;
   const float inv_dim = 1.0f / (float)dim;
   const int64_t step = (int64_t)gridDim.x * blockDim.y, first = (int64_t)blockIdx.x * blockDim.y + group;
   const bool leader = tid == 0;
@@ -158,7 +178,7 @@ __global__ void __launch_bounds__(512, 1) rms_norm_ring_kernel(NormArgs a) {
     fence_mbar_init();
   }
   __syncthreads();
-  const int part = dim * (kX + (a.r ? kR : 0)), stage_bytes = part * blockDim.y;
+  const int r_at = row_room<V>(dim * kX), part = r_at + (a.r ? row_room<V>(dim * kR) : 0), stage_bytes = part * blockDim.y;
   char* const part0 = stages + part * group;
   bool timed_out = false;
   int64_t fetched = 0;   // by this thread
@@ -166,16 +186,16 @@ __global__ void __launch_bounds__(512, 1) rms_norm_ring_kernel(NormArgs a) {
     if (!leader || timed_out || row >= a.rows) return;
     char* const to = part0 + s * stage_bytes;
     uint64_t* bar = &full[group][s];
-    mbar_arrive_expect_tx(bar, (uint32_t)part);
+    mbar_arrive_expect_tx(bar, row_span<V>(a.x, row * a.xs * kX, dim * kX) + (a.r ? row_span<V>(a.r, row * a.rs * kR, dim * kR) : 0u));
     ++fetched;
-    bulk_load(to, static_cast<const char*>(a.x) + row * a.xs * kX, (uint32_t)dim * kX, bar);
-    if (a.r) bulk_load(to + dim * kX, static_cast<const char*>(a.r) + row * a.rs * kR, (uint32_t)dim * kR, bar);
+    row_load<V>(to, a.x, row * a.xs * kX, dim * kX, bar);
+    if (a.r) row_load<V>(to + r_at, a.r, row * a.rs * kR, dim * kR, bar);
   };
   for (int s = 0; s < S; ++s) fetch(first + s * step, s);
-  float w[VPT][8];
+  float w[VPT][V];
 #pragma unroll
   for (int j = 0; j < VPT; ++j)
-    if (j * tpr + tid < nv) load_w<8>(a.w, a.w_bf16, (int64_t)(j * tpr + tid) * 8, w[j]);
+    if ((j * tpr + tid) * V < dim) load_w<V>(a.w, a.w_bf16, (int64_t)(j * tpr + tid) * V, w[j]);
   int s = 0, phase = 0, parity = 0;
 #pragma unroll 1
   for (int64_t row = first; row - group < a.rows; row += step) {
@@ -185,28 +205,40 @@ __global__ void __launch_bounds__(512, 1) rms_norm_ring_kernel(NormArgs a) {
       *(volatile int*)abort_word = 1;
     }
     const char* const from = part0 + s * stage_bytes;
-    float h[VPT][8];
+    const char *const x = from + row_off<V>(a.x, row * a.xs * kX), *const r = from + r_at + row_off<V>(a.r, row * a.rs * kR);
+    float h[VPT][V];
     float2 part_sum = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const int c = (j * tpr + tid) * 8;
+      if (j * tpr * V >= dim) break;
+      const int c = (j * tpr + tid) * V;
       if (on && c < dim) {
-        load8<X_BF16>(from, c, h[j]);
-        if (a.r) {
-          Raw<8, R_BF16> r;
-          r.load(from + dim * kX, c);
-          r.add(h[j]);   // h = round(h + r)
-          r.store(a.h, row * a.hs + c);
-          r.get(h[j]);
+        load_v<V, X_BF16>(x, c, h[j]);
+        if (a.r) {   // h = round(h + r)
+          if constexpr (V == 8) {
+            Raw<8, R_BF16> raw;
+            raw.load(r, c);
+            raw.add(h[j]);
+            raw.store(a.h, row * a.hs + c);
+            raw.get(h[j]);
+          } else {
+            h[j][0] += load1<R_BF16>(r, c);
+            if constexpr (R_BF16) h[j][0] = __bfloat162float(__float2bfloat16_rn(h[j][0]));
+            store1<R_BF16>(a.h, row * a.hs + c, h[j][0]);
+          }
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[j][e] = 0.0f;
+        for (int e = 0; e < V; ++e) h[j][e] = 0.0f;
       }
+      if constexpr (V == 8) {
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const float2 p = make_float2(h[j][e], h[j][e + 1]);
-        part_sum = __ffma2_rn(p, p, part_sum);
+        for (int e = 0; e < 8; e += 2) {
+          const float2 p = make_float2(h[j][e], h[j][e + 1]);
+          part_sum = __ffma2_rn(p, p, part_sum);
+        }
+      } else {
+        part_sum.x += h[j][0] * h[j][0];
       }
     }
     float sum = part_sum.x + part_sum.y;
@@ -227,24 +259,36 @@ __global__ void __launch_bounds__(512, 1) rms_norm_ring_kernel(NormArgs a) {
     if (on && leader) a.rstd[row] = rstd;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const int c = (j * tpr + tid) * 8;
+      if (j * tpr * V >= dim) break;
+      const int c = (j * tpr + tid) * V;
       const bool ok = on && c < dim;
-      float y[8];
+      float y[V];
+      if constexpr (V == 8) {
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const float2 p = __fmul2_rn(__fmul2_rn(make_float2(h[j][e], h[j][e + 1]), make_float2(rstd, rstd)),
-                                    make_float2(w[j][e], w[j][e + 1]));
-        y[e] = p.x;
-        y[e + 1] = p.y;
+        for (int e = 0; e < 8; e += 2) {
+          const float2 p = __fmul2_rn(__fmul2_rn(make_float2(h[j][e], h[j][e + 1]), make_float2(rstd, rstd)),
+                                      make_float2(w[j][e], w[j][e + 1]));
+          y[e] = p.x;
+          y[e + 1] = p.y;
+        }
+      } else {
+        y[0] = h[j][0] * rstd * w[j][0];
       }
-      if (ok && a.y) store8<X_BF16>(a.y, row * a.ys + c, y);
+      if (ok && a.y) store_v<V, X_BF16>(a.y, row * a.ys + c, y);
       if (a.q) {   // every lane of the warp takes part: lanes past the row count as zeros
-        uint32_t m = ok ? mx_amax8(y) : 0u;
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        uint32_t m;
+        if constexpr (V == 8) {
+          m = ok ? mx_amax8(y) : 0u;
+          m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+          m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        } else {
+          m = __reduce_max_sync(0xffffffffu, ok ? __float_as_uint(y[0]) & 0x7fffffffu : 0u);
+        }
         if (ok) {
           const uint32_t code = mx_scale_code(m);
-          *reinterpret_cast<uint2*>(a.q + row * a.qs + c) = mx_pack8(y, code);
+          uint8_t* const q = a.q + row * a.qs + c;
+          if constexpr (V == 8) *reinterpret_cast<uint2*>(q) = mx_pack8(y, code);
+          else *q = (uint8_t)mx_pack1(y[0], code);
           if ((c & (kMxBlock - 1)) == 0) a.sc[row * a.scs + c / kMxBlock] = (uint8_t)code;
         }
       }
@@ -263,46 +307,11 @@ __global__ void __launch_bounds__(512, 1) rms_norm_ring_kernel(NormArgs a) {
 }
 
 // How a row reaches the threads of the gradient:
-//   kBulk    one bulk copy per row and tensor into a ring of stages, S - 1 rows ahead (V = 8)
-//   kCopies  each thread copies its own accesses ahead, into slots that only it uses (V = 1, where
-//            rows begin on no 16-byte boundary)
-//   kDirect  no copies: a thread loads its accesses, twice (rows too long for the above)
-// 16384 x 4096 bf16 with dh, 537 MB: kBulk 82 us, per-thread copies 116-131 us, kDirect 125 us.
-enum class Feed { kBulk, kCopies, kDirect };
-
-// kCopies: where a thread's VPT accesses of each tensor lie in its slot. Slots are an odd number of
-// words apart, so that a warp's accesses to one place of its slots meet no bank twice.
-template <int VPT, bool DY_BF16, bool H_BF16>
-struct GradSlot {
-  static constexpr int kH = VPT * (DY_BF16 ? 2 : 4), kDh = kH + VPT * (H_BF16 ? 2 : 4);
-  static constexpr int odd(int bytes) { return ((bytes + 3) / 4 | 1) * 4; }
-  static constexpr int kPitch = odd(kDh), kPitchDh = odd(2 * kDh - kH);
-};
-
-// Copies a thread's `mine` elements of a tensor (base: its first, step apart) into its slot:
-// asynchronously if fp32, else through registers, all loads before the first store.
-template <int VPT, bool BF16>
-__device__ __forceinline__ void stage_elements(char* slot, const void* base, int64_t i, int step, int mine) {
-  if constexpr (BF16) {
-    __nv_bfloat16 v[VPT];
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      if (j >= mine) break;
-      v[j] = static_cast<const __nv_bfloat16*>(base)[i + j * step];
-    }
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      if (j >= mine) break;
-      reinterpret_cast<__nv_bfloat16*>(slot)[j] = v[j];
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      if (j >= mine) break;
-      cp_async<4>(slot + j * 4, static_cast<const float*>(base) + i + j * step);
-    }
-  }
-}
+//   kBulk    one bulk copy per row and tensor into a ring of stages, S - 1 rows ahead
+//   kDirect  no copies: a thread loads its accesses, twice (rows too long for the ring)
+// 16384 x 4096 bf16 with dh, 537 MB: kBulk 82 us, asynchronous copies per thread 116-131 us, kDirect
+// 125 us.
+enum class Feed { kBulk, kDirect };
 
 // A row group takes every (gridDim.x * groups)-th row; each thread keeps the weight gradient of its
 // own columns in registers over all of them (in a fixed order), and the blocks' sums are added by
@@ -310,9 +319,8 @@ __device__ __forceinline__ void stage_elements(char* slot, const void* base, int
 template <int V, int VPT, bool DY_BF16, bool H_BF16, Feed FEED, int S>
 __global__ void __launch_bounds__(FEED == Feed::kDirect ? 1024 : 512) rms_norm_grad_kernel(NormGradArgs a) {
   extern __shared__ __align__(128) char slots[];   // the stages; after the rows, [dim] floats with several row groups
-  constexpr bool BULK = FEED == Feed::kBulk, COPIES = FEED == Feed::kCopies;
+  constexpr bool BULK = FEED == Feed::kBulk;
   constexpr int kDy = DY_BF16 ? 2 : 4, kH = H_BF16 ? 2 : 4;
-  using L = GradSlot<VPT, DY_BF16, H_BF16>;
   __shared__ float red[2][32];
   __shared__ uint64_t full[kMaxGroups][kGradStages];
   __shared__ int abort_word[2];   // a wait gave up; never set (for the last waits)
@@ -332,30 +340,22 @@ __global__ void __launch_bounds__(FEED == Feed::kDirect ? 1024 : 512) rms_norm_g
     }
     __syncthreads();
   }
-  // bytes between stages, and this thread's (kCopies) or group's (kBulk) part of one
-  const int part = COPIES ? (a.dh ? L::kPitchDh : L::kPitch) : (int)a.dim * (kDy + (a.dh ? 2 : 1) * kH);
-  const int stage_bytes = part * (COPIES ? tpr * blockDim.y : blockDim.y);
-  char* const part0 = slots + part * (COPIES ? group * tpr + tid : group);
-  const int h_at = COPIES ? L::kH : (int)a.dim * kDy, dh_at = COPIES ? L::kDh : (int)a.dim * (kDy + kH);
-  // place of access j of a tensor of E-byte elements within its region of a part
-  auto at = [&](int j, int e) { return COPIES ? j * e : (j * tpr + tid) * V * e; };
+  // where a group's tensors lie in its part of a stage
+  const int dim = (int)a.dim, h_at = row_room<V>(dim * kDy), dh_at = h_at + row_room<V>(dim * kH);
+  const int part = dh_at + (a.dh ? row_room<V>(dim * kH) : 0), stage_bytes = part * blockDim.y;
+  char* const part0 = slots + part * group;
   auto fetch = [&](int64_t row, int s) {
-    char* const to = part0 + s * stage_bytes;
     if constexpr (BULK) {
       if (!leader || timed_out || row >= a.rows) return;
+      char* const to = part0 + s * stage_bytes;
       uint64_t* bar = &full[group][s];
-      mbar_arrive_expect_tx(bar, (uint32_t)part);
+      const int64_t dy_b = row * a.dys * kDy, h_b = row * a.hs * kH, dh_b = row * a.dhs * kH;
+      mbar_arrive_expect_tx(bar, row_span<V>(a.dy, dy_b, dim * kDy) + row_span<V>(a.h, h_b, dim * kH) +
+                                     (a.dh ? row_span<V>(a.dh, dh_b, dim * kH) : 0u));
       ++fetched;
-      bulk_load(to, static_cast<const char*>(a.dy) + row * a.dys * kDy, (uint32_t)a.dim * kDy, bar);
-      bulk_load(to + h_at, static_cast<const char*>(a.h) + row * a.hs * kH, (uint32_t)a.dim * kH, bar);
-      if (a.dh) bulk_load(to + dh_at, static_cast<const char*>(a.dh) + row * a.dhs * kH, (uint32_t)a.dim * kH, bar);
-    } else if constexpr (COPIES) {
-      if (row < a.rows) {
-        stage_elements<VPT, DY_BF16>(to, a.dy, row * a.dys + tid, tpr, mine);
-        stage_elements<VPT, H_BF16>(to + h_at, a.h, row * a.hs + tid, tpr, mine);
-        if (a.dh) stage_elements<VPT, H_BF16>(to + dh_at, a.dh, row * a.dhs + tid, tpr, mine);
-      }
-      cp_async_commit();
+      row_load<V>(to, a.dy, dy_b, dim * kDy, bar);
+      row_load<V>(to + h_at, a.h, h_b, dim * kH, bar);
+      if (a.dh) row_load<V>(to + dh_at, a.dh, dh_b, dim * kH, bar);
     }
   };
   float dw[VPT][V], w[VPT][V];
@@ -367,20 +367,13 @@ __global__ void __launch_bounds__(FEED == Feed::kDirect ? 1024 : 512) rms_norm_g
 #pragma unroll
     for (int e = 0; e < V; ++e) dw[j][e] = 0.0f;
   }
-  // rstd of this row and the rows ahead; with kCopies it is asked for with the copies of its row,
-  // since a load returns after the per-thread copies that were issued before it
-  constexpr int R = COPIES ? S - 1 : 1;
-  float rstds[R];
-#pragma unroll
-  for (int k = 0; k < R; ++k) rstds[k] = first + k * step < a.rows ? a.rstd[first + k * step] : 0.0f;
+  float rstd_next = first < a.rows ? a.rstd[first] : 0.0f;
   int s = 0, phase = 0, parity = 0;
 #pragma unroll 1
   for (int64_t row = first; row - group < a.rows; row += step) {
     const bool on = row < a.rows;
-    const float rstd = rstds[0];
-#pragma unroll
-    for (int k = 0; k + 1 < R; ++k) rstds[k] = rstds[k + 1];
-    rstds[R - 1] = row + R * step < a.rows ? a.rstd[row + R * step] : 0.0f;
+    const float rstd = rstd_next;
+    rstd_next = row + step < a.rows ? a.rstd[row + step] : 0.0f;
     const char* const from = part0 + s * stage_bytes;
     const int previous = s == 0 ? S - 1 : s - 1;
     if constexpr (BULK) {
@@ -388,17 +381,16 @@ __global__ void __launch_bounds__(FEED == Feed::kDirect ? 1024 : 512) rms_norm_g
         timed_out = true;
         *(volatile int*)abort_word = 1;
       }
-    } else if constexpr (COPIES) {
-      fetch(row + (S - 1) * step, previous);
-      cp_async_wait<S - 1>();
     }
+    const char *const dy_row = from + row_off<V>(a.dy, row * a.dys * kDy), *const h_row = from + h_at + row_off<V>(a.h, row * a.hs * kH),
+               *const dh_row = from + dh_at + row_off<V>(a.dh, row * a.dhs * kH);
     constexpr int KEEP = FEED == Feed::kDirect ? 1 : VPT;
     float g[KEEP][V], n[KEEP][V];
     // dy and h of access j (and its weights, where they are not kept)
     auto read = [&](int j, float (&gj)[V], float (&nj)[V]) {
       if constexpr (FEED != Feed::kDirect) {
-        load_v<V, DY_BF16>(from + at(j, kDy), 0, gj);
-        load_v<V, H_BF16>(from + h_at + at(j, kH), 0, nj);
+        load_v<V, DY_BF16>(dy_row, (j * tpr + tid) * V, gj);
+        load_v<V, H_BF16>(h_row, (j * tpr + tid) * V, nj);
       } else {
         const int64_t c = (int64_t)(j * tpr + tid) * V;
         load_v<V, DY_BF16>(a.dy, row * a.dys + c, gj);
@@ -455,7 +447,7 @@ __global__ void __launch_bounds__(FEED == Feed::kDirect ? 1024 : 512) rms_norm_g
         const int64_t col = (int64_t)(j * tpr + tid) * V;
         if (a.dh) {
           float r[V];
-          if constexpr (FEED != Feed::kDirect) load_v<V, H_BF16>(from + dh_at + at(j, kH), 0, r);
+          if constexpr (FEED != Feed::kDirect) load_v<V, H_BF16>(dh_row, (j * tpr + tid) * V, r);
           else load_v<V, H_BF16>(a.dh, row * a.dhs + col, r);
 #pragma unroll
           for (int e = 0; e < V; ++e) d[e] += r[e];
@@ -551,20 +543,21 @@ bool aligned8(const void* p, int64_t stride, int bf16) {
 constexpr int kRingSmem = 220 * 1024;   // of an SM, for the stages of its blocks
 
 // One block of 512 threads per SM, whose stages (at most 64 KB each) always fit.
-template <bool X, bool R>
+template <int V, bool X, bool R>
 cudaError_t norm_ring(const NormArgs& a, cudaStream_t st) {
   static PerDeviceOnce once;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   e = (cudaError_t)once.run(dev, [&] {
-    return (int)cudaFuncSetAttribute(rms_norm_ring_kernel<X, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
+    return (int)cudaFuncSetAttribute(rms_norm_ring_kernel<V, X, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
   });
   if (e != cudaSuccess) return e;
-  const RowShape s = row_shape(a.dim / 8, 2, 512);
+  const RowShape s = row_shape(a.dim / V, V == 8 ? 2 : 16, 512);
   const int64_t groups = (a.rows + s.groups - 1) / s.groups;
-  const size_t smem = (size_t)(kRingStages * s.groups * a.dim * ((X ? 2 : 4) + (a.r ? (R ? 2 : 4) : 0)));
-  rms_norm_ring_kernel<X, R><<<(unsigned)(groups < kSms ? groups : kSms), dim3(s.tpr, s.groups), smem, st>>>(a);
+  const int dim = (int)a.dim;
+  const size_t smem = (size_t)kRingStages * s.groups * (row_room<V>(dim * (X ? 2 : 4)) + (a.r ? row_room<V>(dim * (R ? 2 : 4)) : 0));
+  rms_norm_ring_kernel<V, X, R><<<(unsigned)(groups < kSms ? groups : kSms), dim3(s.tpr, s.groups), smem, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -601,23 +594,23 @@ cudaError_t norm_grad_one(const NormGradArgs& a, RowShape s, int64_t stage, int 
 // Blocks of 256 threads (512 for the longest rows), two per SM where their four stages leave room
 // (4096 columns of fp32 with dh, one block with four stages or two with two: 84 and 91 us for 8192
 // rows; bf16, 16384 rows, two with four, one with four, two with two: 85, 121 and 116 us).
-template <int V, int VPT, bool D, bool H, Feed F>
+template <int V, int VPT, bool D, bool H>
 cudaError_t norm_grad_stages(const NormGradArgs& a, int* blocks, cudaStream_t st) {
   const RowShape s = row_shape(a.dim / V, VPT, 256);
-  const int64_t stage = F == Feed::kBulk
-                            ? s.groups * a.dim * ((D ? 2 : 4) + (a.dh ? 2 : 1) * (H ? 2 : 4))
-                            : s.groups * s.tpr * (a.dh ? GradSlot<VPT, D, H>::kPitchDh : GradSlot<VPT, D, H>::kPitch);
+  const int dim = (int)a.dim, h = row_room<V>(dim * (H ? 2 : 4));
+  const int64_t stage = (int64_t)s.groups * (row_room<V>(dim * (D ? 2 : 4)) + (a.dh ? 2 : 1) * h);
   const int64_t fit = kRingSmem / (kGradStages * stage), most = s.tpr <= 256 ? 2 : 1;
-  if (fit >= 1) return norm_grad_one<V, VPT, D, H, F, kGradStages>(a, s, stage, (int)(fit < most ? fit : most), blocks, st);
-  return norm_grad_one<V, VPT, D, H, F, 2>(a, s, stage, 1, blocks, st);
+  if (fit >= 1)
+    return norm_grad_one<V, VPT, D, H, Feed::kBulk, kGradStages>(a, s, stage, (int)(fit < most ? fit : most), blocks, st);
+  return norm_grad_one<V, VPT, D, H, Feed::kBulk, 2>(a, s, stage, 1, blocks, st);
 }
 
 template <bool D, bool H>
 cudaError_t norm_grad_shapes(const NormGradArgs& a, bool v8, int* blocks, cudaStream_t st) {
-  if (v8 && a.dim <= 8192) return norm_grad_stages<8, 2, D, H, Feed::kBulk>(a, blocks, st);
+  if (v8 && a.dim <= 8192) return norm_grad_stages<8, 2, D, H>(a, blocks, st);
   if (v8) return norm_grad_one<8, 4, D, H, Feed::kDirect, 1>(a, row_shape(a.dim / 8, 4, 256), 0, 1, blocks, st);
-  if (a.dim <= 4096) return norm_grad_stages<1, 8, D, H, Feed::kCopies>(a, blocks, st);
-  if (a.dim <= 8192) return norm_grad_stages<1, 16, D, H, Feed::kCopies>(a, blocks, st);
+  if (a.dim <= 4096) return norm_grad_stages<1, 8, D, H>(a, blocks, st);
+  if (a.dim <= 8192) return norm_grad_stages<1, 16, D, H>(a, blocks, st);
   return norm_grad_one<1, 32, D, H, Feed::kDirect, 1>(a, row_shape(a.dim, 32, 256), 0, 1, blocks, st);
 }
 
@@ -637,9 +630,13 @@ cudaError_t launch_rms_norm(const NormArgs& a, int x_bf16, int r_bf16, int sms, 
   // from 2^22 elements on the ring is no slower (us, bf16 with residual, y and checkpoint, ring and
   // not: 1024 x 4096 10.0 and 9.9, 4096 x 4096 27 and 32, 16384 x 4096 93 and 112, 1024 x 8192 15 and
   // 19); below, starting it costs up to 1 us more (64 x 4096 3.6 and 2.9)
-  if (v8 && a.dim <= 8192 && a.rows * a.dim >= (int64_t(1) << 22)) {
-    if (x_bf16) return r_bf16 ? norm_ring<true, true>(a, st) : norm_ring<true, false>(a, st);
-    return r_bf16 ? norm_ring<false, true>(a, st) : norm_ring<false, false>(a, st);
+  if (a.dim <= 8192 && a.rows * a.dim >= (int64_t(1) << 22)) {
+    if (v8) {
+      if (x_bf16) return r_bf16 ? norm_ring<8, true, true>(a, st) : norm_ring<8, true, false>(a, st);
+      return r_bf16 ? norm_ring<8, false, true>(a, st) : norm_ring<8, false, false>(a, st);
+    }
+    if (x_bf16) return r_bf16 ? norm_ring<1, true, true>(a, st) : norm_ring<1, true, false>(a, st);
+    return r_bf16 ? norm_ring<1, false, true>(a, st) : norm_ring<1, false, false>(a, st);
   }
   if (v8) {
     const RowShape s = row_shape(a.dim / 8, a.rows < 2 * sms ? 1 : 2, 128);
