@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(NormArgs a) {
 // come by one bulk copy each into a ring of stages, S rows ahead (a row lies in registers once its sum
 // is taken, and frees its stage). Three rows ahead of two groups of 4096 columns, 96 KB per SM, suffice:
 // with 192 KB (three blocks of four) 16384 x 4096 takes 118 us instead of 95.
-constexpr int kMaxGroups = 16, kRingStages = 3, kGradStages = 4;
+constexpr int kMaxGroups = 32, kRingStages = 3, kGradStages = 4;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 // A row of n bytes at p by bulk copy: the 16-byte granules that hold it, of which it begins at byte
@@ -161,9 +161,9 @@ __device__ __forceinline__ void row_load(void* to, const void* base, int64_t byt
 }
 
 template <int V, bool X_BF16, bool R_BF16>
-__global__ void __launch_bounds__(512, 1) rms_norm_ring_kernel(NormArgs a) {
+__global__ void __launch_bounds__(V == 8 ? 512 : 1024, 1) rms_norm_ring_kernel(NormArgs a) {
   extern __shared__ __align__(128) char stages[];
-  constexpr int VPT = V == 8 ? 2 : 16, S = kRingStages, kX = X_BF16 ? 2 : 4, kR = R_BF16 ? 2 : 4;
+  constexpr int VPT = V == 8 ? 2 : 8, S = kRingStages, kX = X_BF16 ? 2 : 4, kR = R_BF16 ? 2 : 4;
   __shared__ float red[2][32];
   __shared__ uint64_t full[kMaxGroups][S];
   __shared__ int abort_word[2];   // a wait gave up; never set (for the last waits)
@@ -542,7 +542,8 @@ bool aligned8(const void* p, int64_t stride, int bf16) {
 
 constexpr int kRingSmem = 220 * 1024;   // of an SM, for the stages of its blocks
 
-// One block of 512 threads per SM, whose stages (at most 64 KB each) always fit.
+// One block per SM, whose stages (at most 64 KB each) always fit: of 512 threads with 16 elements each,
+// or of 1024 with 8 where they take single accesses.
 template <int V, bool X, bool R>
 cudaError_t norm_ring(const NormArgs& a, cudaStream_t st) {
   static PerDeviceOnce once;
@@ -553,7 +554,7 @@ cudaError_t norm_ring(const NormArgs& a, cudaStream_t st) {
     return (int)cudaFuncSetAttribute(rms_norm_ring_kernel<V, X, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
   });
   if (e != cudaSuccess) return e;
-  const RowShape s = row_shape(a.dim / V, V == 8 ? 2 : 16, 512);
+  const RowShape s = V == 8 ? row_shape(a.dim / 8, 2, 512) : row_shape(a.dim, 8, 1024);
   const int64_t groups = (a.rows + s.groups - 1) / s.groups;
   const int dim = (int)a.dim;
   const size_t smem = (size_t)kRingStages * s.groups * (row_room<V>(dim * (X ? 2 : 4)) + (a.r ? row_room<V>(dim * (R ? 2 : 4)) : 0));
