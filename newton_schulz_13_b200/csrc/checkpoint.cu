@@ -2,8 +2,8 @@
 //
 // Bound by HBM: 2 or 4 bytes read and 1 + 1/32 written per element on the way in, the reverse on
 // the way out (8192 x 14336 bf16: 57 us stored, 53 restored, 6.3 and 6.7 TB/s). Aligned rows: a thread
-// owns eight consecutive elements of two places, four lanes a 32-element block; other rows: a lane
-// owns one element of eight blocks, a warp those blocks (8000 x 4093 bf16: 92 and 65 us).
+// owns eight consecutive elements of two places, four lanes a 32-element block; other rows: four
+// elements of four places, eight lanes a block.
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -51,28 +51,44 @@ __global__ void __launch_bounds__(kThreads) mx_store_kernel(MxArgs a, Div per_ro
   }
 }
 
-// Any rows: a warp takes kAny blocks of 32, a lane one element of each, all loads before the first
-// store (with one block per warp the kernels wait on latency: 3000 x 13001 restored in 159 us).
-constexpr int kAny = 8;
+// Any rows: a thread has four consecutive elements of kQuad places, eight lanes a 32-element block.
+// per_row: four-element groups of a row, padded to whole blocks (a multiple of 8).
+constexpr int kQuad = 4;
 
 template <bool X_BF16>
 __global__ void __launch_bounds__(kThreads) mx_store_any_kernel(MxArgs a, Div per_row, uint32_t total) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t b0 = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kAny;
-  float v[kAny];
+  const uint32_t t0 = blockIdx.x * (kQuad * kThreads) + threadIdx.x;
+  float v[kQuad][4];
 #pragma unroll
-  for (int j = 0; j < kAny; ++j) {
-    const uint32_t b = b0 + j, row = per_row.quot(b), c = (b - row * per_row.d) * 32 + lane;
-    v[j] = b < total && c < a.dim ? load1<X_BF16>(a.x, (int64_t)row * a.xs + c) : 0.0f;
+  for (int j = 0; j < kQuad; ++j) {
+    const uint32_t t = t0 + j * kThreads, row = per_row.quot(t), c = (t - row * per_row.d) * 4;
+    if (t < total && c < a.dim) load4_any<X_BF16>(a.x, (int64_t)row * a.xs + c, a.dim - c, v[j]);
+    else v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0.0f;
   }
 #pragma unroll
-  for (int j = 0; j < kAny; ++j) {
-    const uint32_t b = b0 + j, row = per_row.quot(b), blk = b - row * per_row.d, c = blk * 32 + lane;
-    if (b >= total) break;
-    const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(v[j]) & 0x7fffffffu);
+  for (int j = 0; j < kQuad; ++j) {
+    const uint32_t t = t0 + j * kThreads, row = per_row.quot(t), c = (t - row * per_row.d) * 4;
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = max(m, __float_as_uint(v[j][e]) & 0x7fffffffu);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (t >= total || c >= a.dim) continue;
     const uint32_t code = mx_scale_code(m);
-    if (c < a.dim) a.q[(int64_t)row * a.qs + c] = (uint8_t)mx_pack1(v[j], code);
-    if (lane == 0) a.sc[(int64_t)row * a.scs + blk] = (uint8_t)code;
+    uint32_t w = 0x7f7f7f7fu;
+    if (code != kMxNan) {
+      const float s = mx_inv_scale(code);
+      w = mx_pack2(v[j][0] * s, v[j][1] * s) | (mx_pack2(v[j][2] * s, v[j][3] * s) << 16);
+    }
+    uint8_t* const q = a.q + (int64_t)row * a.qs + c;
+    if (c + 4 <= a.dim && ((uintptr_t)q & 3) == 0) {
+      *reinterpret_cast<uint32_t*>(q) = w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < a.dim) q[e] = (uint8_t)(w >> (8 * e));
+    }
+    if (!(c & (kMxBlock - 1))) a.sc[(int64_t)row * a.scs + c / kMxBlock] = (uint8_t)code;
   }
 }
 
@@ -112,12 +128,10 @@ __global__ void __launch_bounds__(kThreads) mx_restore_kernel(MxArgs a, Div per_
   }
 }
 
-// Codes at any address into rows aligned to four elements (a weight gradient's workspace): a thread
-// has four elements of kQuad places, from the two aligned words that hold their codes.
-constexpr int kQuad = 4;
-
+// Any rows: a thread has four elements of kQuad places, from the two aligned words that hold their
+// codes; out4: groups of four of out are aligned.
 template <bool O_BF16>
-__global__ void __launch_bounds__(kThreads) mx_restore_out_kernel(MxArgs a, Div per_row, uint32_t total) {
+__global__ void __launch_bounds__(kThreads) mx_restore_any_kernel(MxArgs a, Div per_row, uint32_t total, int out4) {
   grid_launch_dependents();
   zero_words(a);
   const uint32_t t0 = blockIdx.x * (kQuad * kThreads) + threadIdx.x;
@@ -142,40 +156,13 @@ __global__ void __launch_bounds__(kThreads) mx_restore_out_kernel(MxArgs a, Div 
     const float2 lo = mx_unpack2(w[j]), hi = mx_unpack2(w[j] >> 16);
     const float v[4] = {lo.x * s, lo.y * s, hi.x * s, hi.y * s};
     const int64_t to = (int64_t)row * a.xs + c;
-    if (c + 4 <= a.dim) {
-      if constexpr (O_BF16) {
-        const __nv_bfloat162 x = __floats2bfloat162_rn(v[0], v[1]), y = __floats2bfloat162_rn(v[2], v[3]);
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + to) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-      } else {
-        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) = make_float4(v[0], v[1], v[2], v[3]);
-      }
+    if (out4 && c + 4 <= a.dim) {
+      store4<O_BF16>(a.out, to, v);
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (c + e < a.dim) store1<O_BF16>(a.out, to + e, v[e]);
     }
-  }
-}
-
-template <bool O_BF16>
-__global__ void __launch_bounds__(kThreads) mx_restore_any_kernel(MxArgs a, Div per_row, uint32_t total) {
-  grid_launch_dependents();
-  zero_words(a);
-  const int lane = threadIdx.x & 31;
-  const uint32_t b0 = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kAny;
-  uint8_t q[kAny], code[kAny];
-#pragma unroll
-  for (int j = 0; j < kAny; ++j) {
-    const uint32_t b = b0 + j, row = per_row.quot(b), blk = b - row * per_row.d, c = blk * 32 + lane;
-    const bool ok = b < total && c < a.dim;
-    q[j] = ok ? a.q[(int64_t)row * a.qs + c] : 0;
-    code[j] = ok ? a.sc[(int64_t)row * a.scs + blk] : 0;
-  }
-#pragma unroll
-  for (int j = 0; j < kAny; ++j) {
-    const uint32_t b = b0 + j, row = per_row.quot(b), c = (b - row * per_row.d) * 32 + lane;
-    if (b < total && c < a.dim) store1<O_BF16>(a.out, (int64_t)row * a.xs + c, mx_unpack1(q[j]) * mx_scale(code[j]));
   }
 }
 
@@ -196,8 +183,8 @@ MxArgs flat(MxArgs a) {
 
 // Launches over all rows, `per_row` work items each and `per_block` of them per block, in
 // runs of rows that keep the item index below 2^31.
-template <class K>
-cudaError_t launch_rows(MxArgs a, int64_t x_size, int64_t per_row, int64_t per_block, K kernel, cudaStream_t s) {
+template <class K, class... More>
+cudaError_t launch_rows(MxArgs a, int64_t x_size, int64_t per_row, int64_t per_block, cudaStream_t s, K kernel, More... more) {
   const int64_t most = ((int64_t(1) << 31) - 1) / per_row;
   for (int64_t r = 0; r < a.rows; r += most) {
     MxArgs b = a;
@@ -207,7 +194,7 @@ cudaError_t launch_rows(MxArgs a, int64_t x_size, int64_t per_row, int64_t per_b
     b.q = a.q + r * a.qs;
     b.sc = a.sc + r * a.scs;
     const int64_t total = b.rows * per_row;
-    kernel<<<(unsigned)((total + per_block - 1) / per_block), kThreads, 0, s>>>(b, Div((uint32_t)per_row), (uint32_t)total);
+    kernel<<<(unsigned)((total + per_block - 1) / per_block), kThreads, 0, s>>>(b, Div((uint32_t)per_row), (uint32_t)total, more...);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -219,17 +206,17 @@ cudaError_t launch_rows(MxArgs a, int64_t x_size, int64_t per_row, int64_t per_b
 cudaError_t launch_mx_store(const MxArgs& args, int x_bf16, cudaStream_t s) {
   const MxArgs a = flat(args);
   const int64_t size = x_bf16 ? 2 : 4, blocks = (a.dim + 31) / 32;
-  if (vec8(a, a.x)) return launch_rows(a, size, blocks * 4, kAcc * kThreads, x_bf16 ? mx_store_kernel<true> : mx_store_kernel<false>, s);
-  return launch_rows(a, size, blocks, kAny * kThreads / 32, x_bf16 ? mx_store_any_kernel<true> : mx_store_any_kernel<false>, s);
+  if (vec8(a, a.x)) return launch_rows(a, size, blocks * 4, kAcc * kThreads, s, x_bf16 ? mx_store_kernel<true> : mx_store_kernel<false>);
+  return launch_rows(a, size, blocks * 8, kQuad * kThreads, s, x_bf16 ? mx_store_any_kernel<true> : mx_store_any_kernel<false>);
 }
 
 cudaError_t launch_mx_restore(const MxArgs& args, int out_bf16, cudaStream_t s) {
   const MxArgs a = flat(args);
-  const int64_t size = out_bf16 ? 2 : 4, blocks = (a.dim + 31) / 32;
-  if (vec8(a, a.out)) return launch_rows(a, size, a.dim / 8, kAcc * kThreads, out_bf16 ? mx_restore_kernel<true> : mx_restore_kernel<false>, s);
-  if ((uintptr_t)a.out % 16 == 0 && a.xs % 4 == 0)
-    return launch_rows(a, size, (a.dim + 3) / 4, kQuad * kThreads, out_bf16 ? mx_restore_out_kernel<true> : mx_restore_out_kernel<false>, s);
-  return launch_rows(a, size, blocks, kAny * kThreads / 32, out_bf16 ? mx_restore_any_kernel<true> : mx_restore_any_kernel<false>, s);
+  const int64_t size = out_bf16 ? 2 : 4;
+  if (vec8(a, a.out)) return launch_rows(a, size, a.dim / 8, kAcc * kThreads, s, out_bf16 ? mx_restore_kernel<true> : mx_restore_kernel<false>);
+  const int out4 = (uintptr_t)a.out % 16 == 0 && a.xs % 4 == 0;
+  return launch_rows(a, size, (a.dim + 3) / 4, kQuad * kThreads, s, out_bf16 ? mx_restore_any_kernel<true> : mx_restore_any_kernel<false>,
+                     out4);
 }
 
 }  // namespace muon

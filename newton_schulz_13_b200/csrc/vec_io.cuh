@@ -119,6 +119,38 @@ struct Raw<1, false> {
   __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = r; }
 };
 
+// Four consecutive elements at any element index, zeros past the `left` that remain in the row (at
+// least one). bf16 come in the aligned words that hold them; each word read holds one that remains.
+template <bool BF16>
+__device__ __forceinline__ void load4_any(const void* base, int64_t idx, int64_t left, float (&v)[4]) {
+  if constexpr (BF16) {
+    const uintptr_t p = (uintptr_t)(static_cast<const __nv_bfloat16*>(base) + idx), off = p & 2;
+    const uint32_t* const at = reinterpret_cast<const uint32_t*>(p - off);
+    const int64_t bytes = left * 2 + (int64_t)off;
+    const uint32_t w0 = at[0], w1 = bytes > 4 ? at[1] : 0u, w2 = off && bytes > 8 ? at[2] : 0u;
+    const uint32_t a = __funnelshift_r(w0, w1, off * 8), b = __funnelshift_r(w1, w2, off * 8);
+    v[0] = __uint_as_float(a << 16);
+    v[1] = left > 1 ? __uint_as_float(a & 0xffff0000u) : 0.0f;
+    v[2] = left > 2 ? __uint_as_float(b << 16) : 0.0f;
+    v[3] = left > 3 ? __uint_as_float(b & 0xffff0000u) : 0.0f;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = e < left ? static_cast<const float*>(base)[idx + e] : 0.0f;
+  }
+}
+
+// Four elements at an index aligned to four.
+template <bool BF16>
+__device__ __forceinline__ void store4(void* base, int64_t idx, const float (&v)[4]) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(base) + idx) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  } else {
+    *reinterpret_cast<float4*>(static_cast<float*>(base) + idx) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+}
+
 // V = 8 or 1 elements, for kernels that serve aligned and unaligned rows with one body.
 template <int V, bool BF16>
 __device__ __forceinline__ void load_v(const void* base, int64_t idx, float (&v)[V]) {

@@ -87,17 +87,6 @@ __device__ __forceinline__ float4 load4(const void* p, int64_t at) {
   }
 }
 
-template <bool BF16>
-__device__ __forceinline__ void store4(void* p, int64_t at, const float4& f) {
-  if constexpr (BF16) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(f.x, f.y), b = __floats2bfloat162_rn(f.z, f.w);
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + at) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  } else {
-    *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = f;
-  }
-}
-
 // An epilogue warp's 32 rows x 32 columns of grad (rows x cols of them exist) go through its 4 KB of
 // shared memory. 16-byte chunk c of row r lies at chunk c ^ (r & 7) of its row: eight lanes that
 // have a row's 32 columns, and lanes that each have a row, meet no bank twice. `at` is the place of
@@ -117,7 +106,10 @@ __device__ __forceinline__ void block_out(const ProductArgs& a, int64_t at, int 
     const int sub = lane >> 3, chunk = lane & 7;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      store4<BF16>(a.grad, at + (4 * i + sub) * a.gs + chunk * 4, stg[(4 * i + sub) * 8 + (chunk ^ ((4 * i + sub) & 7))]);
+    {
+      const float4 f = stg[(4 * i + sub) * 8 + (chunk ^ ((4 * i + sub) & 7))];
+      store4<BF16>(a.grad, at + (4 * i + sub) * a.gs + chunk * 4, {f.x, f.y, f.z, f.w});
+    }
   } else if (lane < cols) {
 #pragma unroll 8
     for (int r = 0; r < rows; ++r)
@@ -487,8 +479,7 @@ __global__ void __launch_bounds__(256) wgrad_zero_kernel(void* grad, int64_t gs,
 
 // Copies dy into bf16 rows of `pitch` elements (a multiple of 8); an fp32 dy into three planes,
 // plane_rows apart. A thread has kStageAcc groups of V columns, 256 groups apart, all loaded before
-// the first is stored: V = 8 where dy's rows are aligned, else 4, and then bf16 come in the aligned
-// words that hold them. per_row: groups of a row (the last may end in the padding), total: of all
+// the first is stored: V = 8 where dy's rows are aligned, else 4. per_row: groups of a row (the last may end in the padding), total: of all
 // rows, below 2^31.
 template <int V>
 constexpr int kStageAcc = V == 8 ? 1 : 4;
@@ -505,28 +496,15 @@ __global__ void __launch_bounds__(256) wgrad_stage_dy_kernel(const void* dy, int
     if (i >= total) continue;
     if constexpr (V == 8) {
       load8<DY_BF16>(dy, t * dys + c, all[j]);
-    } else if constexpr (DY_BF16) {
-      const uintptr_t p = (uintptr_t)(static_cast<const __nv_bfloat16*>(dy) + t * dys + c), off = p & 2;
-      const uint32_t* const at = reinterpret_cast<const uint32_t*>(p - off);
-      // bytes from `at` to the row's end; a word that begins before it holds an element of the row
-      const int64_t left = (n - c) * 2 + (int64_t)off;
-      const uint32_t w0 = at[0], w1 = left > 4 ? at[1] : 0u, w2 = off && left > 8 ? at[2] : 0u;
-      const uint32_t a = __funnelshift_r(w0, w1, off * 8), b = __funnelshift_r(w1, w2, off * 8);
-      all[j][0] = __uint_as_float(a << 16);
-      all[j][1] = __uint_as_float(a & 0xffff0000u);
-      all[j][2] = __uint_as_float(b << 16);
-      all[j][3] = __uint_as_float(b & 0xffff0000u);
     } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e) all[j][e] = c + e < n ? static_cast<const float*>(dy)[t * dys + c + e] : 0.0f;
+      load4_any<DY_BF16>(dy, t * dys + c, n - c, all[j]);
     }
   }
   auto put = [&](int64_t to, const float (&v)[V]) {
     if constexpr (V == 8) {
       store8<true>(out, to, v);
     } else {
-      const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-      *reinterpret_cast<uint2*>(out + to) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+      store4<true>(out, to, v);
     }
   };
 #pragma unroll
