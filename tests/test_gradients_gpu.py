@@ -695,6 +695,46 @@ def test_graphs_and_streams():
     assert ns.check_status() == ns.OK
 
 
+@pytest.mark.parametrize("dim", [4096, 4095])
+def test_offsets_past_32_bits(dim):
+    """Matrices of over 2^31 elements: their last rows give what those rows give alone."""
+    import newton_schulz_13_b200 as ns
+    rows, tail = 530_000, 40
+    last = normal((tail, dim), BF16, 130)
+    x = torch.zeros(rows, dim, dtype=BF16, device="cuda")
+    x[-tail:] = last
+    assert x.numel() > 1 << 31
+    w = torch.ones(dim, device="cuda")
+    ck, ref = ns.checkpoint_store(x), ns.checkpoint_store(last)
+    assert torch.equal(ck.q[-tail:].view(torch.uint8), ref.q.view(torch.uint8))
+    assert torch.equal(ck.scales[-tail:].view(torch.uint8), ref.scales.view(torch.uint8))
+    back = ns.checkpoint_restore(ck)
+    assert torch.equal(back[-tail:], ns.checkpoint_restore(ref)) and not back[:-tail].any()
+    del back
+    f, g = ns.rms_norm(x, w, checkpoint=True), ns.rms_norm(last, w, checkpoint=True)
+    each = U[BF16] + SUM * E     # the two may take different kernels: the orders of their sums differ
+    within(f.y[-tail:], g.y.double(), 2 * each * g.y.double().abs())
+    assert not f.y[:-tail].any()
+    dx, dw = ns.rms_norm_grad(x, x, w, f.rstd)
+    want, want_w = ns.rms_norm_grad(last, last, w, f.rstd[-tail:])
+    assert torch.equal(dx[-tail:], want) and not dx[:-tail].any()
+    terms = (last.double() ** 2 * f.rstd[-tail:].double()[:, None]).sum(0)
+    within(dw, want_w.double(), 2 * (tail + 8) * E * terms)
+    del f, dx
+    t = torch.arange(rows - tail, rows, device="cuda")
+    assert torch.equal(ns.embedding(t, x), last)
+    grad = ns.embedding_grad(t, last, rows)
+    assert torch.equal(grad[-tail:], last) and not grad[:-tail].any()
+    grad = ns.embedding_grad(t, last, rows, grad=grad, accumulate=True)
+    assert torch.equal(grad[-tail:].float(), 2 * last.float())
+    del grad
+    # a checkpoint of ones: sums of ones are exact
+    ones = ns.checkpoint_store(x.fill_(1.0))
+    dy = torch.ones(rows, 8, dtype=BF16, device="cuda")
+    assert torch.equal(ns.weight_grad(dy, ones, grad_dtype=FP32), torch.full((8, dim), float(rows), device="cuda"))
+    assert ns.check_status() == ns.OK
+
+
 def test_plain_calls_and_full_path_agree(monkeypatch):
     """Calls that take the extension's path give what the path through ctypes gives."""
     import newton_schulz_13_b200 as ns
