@@ -210,14 +210,17 @@ MUON_API int muon_adamw_step(int count, float* const* params, const void* const*
  *
  * Matrices here are row-major with contiguous rows; a *_stride is the distance between rows in
  * elements, at least the row length. Rows that are multiples of 8 elements, 16-byte aligned, take
- * the fast paths; any other alignment and width is accepted. Workspaces are the caller's: device
+ * the fast paths; any other alignment and width is accepted (such rows may be read by the aligned 16
+ * bytes that hold their ends; what these hold of others is not used). Workspaces are the caller's: device
  * memory, 256-byte aligned, at least as large as the *_workspace call says (that call needs no
  * device; it returns bytes, or a negative error code), free for other use once the call's work on
  * the stream is done. These calls allocate nothing, keep nothing between calls and may be captured
  * into graphs and run concurrently on several streams with workspaces of their own; make a
  * process's first call on a device outside a capture. Outputs may overlap no other buffer, except
  * where a call says so. Sums and statistics are fp32, in an order that does not change from run to
- * run. These launches count in muon_launch_count; muon_profile_read does not time them.
+ * run. Waits inside the kernels are bounded as in muon_step (muon_set_wait_limit_ns,
+ * muon_check_status). These launches count in muon_launch_count; muon_profile_read does not time
+ * them.
  * ------------------------------------------------------------------------------------------- */
 
 /*
@@ -234,7 +237,8 @@ MUON_API int muon_embedding(const void* tokens, int token_bits, int64_t n, const
 /*
  * Its gradient by the table, from sorted tokens:
  *   grad[v][:] = (accumulate ? grad[v][:] : 0) + scale * sum over t with id_t = v of dy[t][:]
- * summed in fp32 in the order of t and rounded once. Without accumulate every row of grad is
+ * summed in fp32 and rounded once, in an order that goes by the places t alone (an id's first 8
+ * places in their order, the next 8, and so on; then these sums by eights). Without accumulate every row of grad is
  * written (zeros for absent tokens); with it, the rows of absent tokens are not touched. Ids
  * outside [0, vocab) contribute nothing (ids >= vocab are reported as above).
  */
@@ -295,8 +299,7 @@ MUON_API int muon_checkpoint_restore(const void* codes, int64_t codes_stride, co
  * Weight gradient of y = x W^T from dy and the checkpoint of x:
  *   grad[i][j] = (accumulate ? grad[i][j] : 0) + sum over t of dy[t][i] x[t][j],  i < n, j < k
  * on the tensor cores. An fp32 dy enters as three bf16 terms that sum to it exactly. rows <= 2^29,
- * n and k <= 2^20; rows = 0 gives zeros (or leaves grad, accumulating). Waits inside the kernel are
- * bounded as in muon_step (muon_set_wait_limit_ns, muon_check_status).
+ * n and k <= 2^20; rows = 0 gives zeros (or leaves grad, accumulating).
  */
 MUON_API int64_t muon_weight_grad_workspace(int64_t rows, int64_t n, int64_t k, muon_dtype_t dy_dtype);
 MUON_API int muon_weight_grad(const void* dy, muon_dtype_t dy_dtype, int64_t dy_stride, const void* codes,

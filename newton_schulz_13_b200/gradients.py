@@ -213,8 +213,8 @@ def embedding_grad(tokens, dy, vocab: int, scale: float = 1.0, grad=None, grad_d
                    stream=None):
     """Gradient of embedding() by its table: grad[v] = scale * sum of dy over the places of token v,
     [vocab, dim] in grad_dtype (default: dy's), zeros for absent tokens. With accumulate, added to
-    `grad`, of which only the rows of present tokens are touched. The sums are fp32, in the order of
-    the tokens; negative and too large ids contribute nothing."""
+    `grad`, of which only the rows of present tokens are touched. The sums are fp32, in an order that
+    goes by the tokens' places alone; negative and too large ids contribute nothing."""
     if stream is None and _fast is not None:
         got = _fast.embedding_grad(tokens, dy, vocab, scale, grad, grad_dtype, accumulate)
         if got is not None:
