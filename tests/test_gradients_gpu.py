@@ -518,6 +518,36 @@ def test_weight_grad(rows, n, k, dy_dt, grad_dt):
     assert ns.check_status() == ns.OK
 
 
+@pytest.mark.parametrize("shapes", [((8192, 768, 2304), (4096, 1536, 1536)), ((16384, 256, 256), (5000, 2304, 768))])
+def test_weight_grad_joined_tiles_on_two_streams_and_in_graphs(shapes):
+    """Calls whose tiles fall to several pairs, many at once on two streams, beside graphs of them:
+    each gives what it gives alone."""
+    import newton_schulz_13_b200 as ns
+    sets = []
+    for i, (rows, n, k) in enumerate(shapes):
+        dy, ck = normal((rows, n), BF16, 140 + i), ns.checkpoint_store(normal((rows, k), BF16, 150 + i))
+        sets.append((dy, ck, ns.weight_grad(dy, ck, grad_dtype=FP32)))
+    graphs, outs = [], []
+    for dy, ck, _ in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(ns.weight_grad(dy, ck, grad_dtype=FP32))
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for r in range(20):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(ns.weight_grad(sets[i][0], sets[i][1], grad_dtype=FP32))
+                if r % 5 == 4:
+                    graphs[i].replay()
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(g, sets[i][2]) for g in got[i]) and torch.equal(outs[i], sets[i][2])
+    assert ns.check_status() == ns.OK
+
+
 def test_weight_grad_fp32_keeps_its_precision_over_many_rows():
     """The sum over 20,000 rows stays near fp32: 1e-5 of the norm is half of what fp32 outputs of
     such sums may be off by; the truncation of one long running sum would exceed it."""
