@@ -616,7 +616,7 @@ cudaError_t norm_grad_shapes(const NormGradArgs& a, bool v8, int* blocks, cudaSt
 }
 
 int norm_grad_blocks(int64_t rows) {
-  const int64_t cap = (int64_t)kSms * 4;
+  const int64_t cap = (int64_t)kSms * 2;   // two blocks per SM at most
   return (int)(rows < cap ? rows : cap);
 }
 
