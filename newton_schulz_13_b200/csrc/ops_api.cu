@@ -274,8 +274,7 @@ int muon_rms_norm_grad(const void* dy, muon_dtype_t dy_dtype, int64_t dy_stride,
     return MUON_OK;
   }
   NormGradArgs a = {};
-  int sms = 0;
-  if (int rc = current_device_info(&sms, &a.status, &a.wait_ns)) return rc;
+  if (int rc = current_device_info(nullptr, &a.status, &a.wait_ns)) return rc;
   a.dy = dy;
   a.h = h;
   a.w = weight;
@@ -293,7 +292,7 @@ int muon_rms_norm_grad(const void* dy, muon_dtype_t dy_dtype, int64_t dy_stride,
   a.accumulate = accumulate != 0;
   a.partial = static_cast<float*>(workspace);
   int64_t launches = 0;
-  const cudaError_t e = launch_rms_norm_grad(a, dy_dtype == MUON_BF16, h_dtype == MUON_BF16, sms, &launches,
+  const cudaError_t e = launch_rms_norm_grad(a, dy_dtype == MUON_BF16, h_dtype == MUON_BF16, &launches,
                                              reinterpret_cast<cudaStream_t>(stream));
   return finish(e, "rms_norm gradient launch", launches);
 }

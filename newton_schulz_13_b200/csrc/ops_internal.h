@@ -72,7 +72,7 @@ struct NormGradArgs {
   uint64_t wait_ns;
 };
 int64_t norm_grad_workspace(int64_t rows, int64_t dim);
-cudaError_t launch_rms_norm_grad(const NormGradArgs& a, int dy_bf16, int h_bf16, int sms, int64_t* launches,
+cudaError_t launch_rms_norm_grad(const NormGradArgs& a, int dy_bf16, int h_bf16, int64_t* launches,
                                  cudaStream_t s);
 
 // ---- 8-bit activation checkpoints

@@ -654,7 +654,7 @@ int64_t norm_grad_workspace(int64_t rows, int64_t dim) {
   return (int64_t)norm_grad_blocks(rows) * dim * (int64_t)sizeof(float);
 }
 
-cudaError_t launch_rms_norm_grad(const NormGradArgs& a, int dy_bf16, int h_bf16, int sms, int64_t* launches,
+cudaError_t launch_rms_norm_grad(const NormGradArgs& a, int dy_bf16, int h_bf16, int64_t* launches,
                                  cudaStream_t st) {
   if (a.rows == 0) {   // the empty sum
     norm_dw_kernel<<<(unsigned)((a.dim + 31) / 32), 1024, 0, st>>>(a.partial, a.dw, 0, a.dim, a.accumulate);
