@@ -91,29 +91,44 @@ __device__ __forceinline__ float4 load4(const void* p, int64_t at) {
 // shared memory. 16-byte chunk c of row r lies at chunk c ^ (r & 7) of its row: eight lanes that
 // have a row's 32 columns, and lanes that each have a row, meet no bank twice. `at` is the place of
 // the first row and column.
+//
+// A lane's eight accesses of whole, aligned blocks: rows 4 i + lane / 8, columns 4 (lane % 8) on.
 template <bool BF16>
-__device__ __forceinline__ void block_in_any(const ProductArgs& a, int64_t at, int rows, int cols, int lane, float4* stg) {
-#pragma unroll 8
-  for (int r = 0; r < 32; ++r)
-    reinterpret_cast<float*>(stg + r * 8 + ((lane >> 2) ^ (r & 7)))[lane & 3] =
-        r < rows && lane < cols ? load1<BF16>(a.grad, at + r * a.gs + lane) : 0.0f;
+__device__ __forceinline__ void block_load(const ProductArgs& a, int64_t at, int lane, float4 (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = load4<BF16>(a.grad, at + (4 * i + (lane >> 3)) * a.gs + (lane & 7) * 4);
+}
+
+__device__ __forceinline__ void block_sums(int lane, const float4* stg, bool add, const float4 (&old)[8], float4 (&v)[8]) {
+  const int sub = lane >> 3, chunk = lane & 7;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = stg[(4 * i + sub) * 8 + (chunk ^ ((4 * i + sub) & 7))];
+    if (add) v[i] = make_float4(v[i].x + old[i].x, v[i].y + old[i].y, v[i].z + old[i].z, v[i].w + old[i].w);
+  }
 }
 
 template <bool BF16>
-__device__ __forceinline__ void block_out(const ProductArgs& a, int64_t at, int rows, int cols, bool fast, int lane,
-                                          const float4* stg) {
-  if (fast) {
-    const int sub = lane >> 3, chunk = lane & 7;
+__device__ __forceinline__ void block_store(const ProductArgs& a, int64_t at, int lane, const float4 (&v)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-    {
-      const float4 f = stg[(4 * i + sub) * 8 + (chunk ^ ((4 * i + sub) & 7))];
-      store4<BF16>(a.grad, at + (4 * i + sub) * a.gs + chunk * 4, {f.x, f.y, f.z, f.w});
+  for (int i = 0; i < 8; ++i)
+    store4<BF16>(a.grad, at + (4 * i + (lane >> 3)) * a.gs + (lane & 7) * 4, {v[i].x, v[i].y, v[i].z, v[i].w});
+}
+
+// Any other block: a lane per column, eight rows at a time.
+template <bool BF16>
+__device__ __forceinline__ void block_out_any(const ProductArgs& a, int64_t at, int rows, int cols, int lane, const float4* stg) {
+  if (lane >= cols) return;
+  for (int r0 = 0; r0 < rows; r0 += 8) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = a.accumulate && r0 + i < rows ? load1<BF16>(a.grad, at + (r0 + i) * a.gs + lane) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = r0 + i;
+      if (r < rows)
+        store1<BF16>(a.grad, at + r * a.gs + lane, v[i] + reinterpret_cast<const float*>(stg + r * 8 + ((lane >> 2) ^ (r & 7)))[lane & 3]);
     }
-  } else if (lane < cols) {
-#pragma unroll 8
-    for (int r = 0; r < rows; ++r)
-      store1<BF16>(a.grad, at + r * a.gs + lane, reinterpret_cast<const float*>(stg + r * 8 + ((lane >> 2) ^ (r & 7)))[lane & 3]);
   }
 }
 
@@ -321,50 +336,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         fast = a.vec && rows == 32 && cols == 32;
         return r0 * a.gs + col0 + g * 32;
       };
-      // the sums begin with the old gradient, whose way here the first MMAs hide
       float sum[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) sum[i] = 0.0f;
-      if (a.accumulate && w.part < 0) {
-        const int sub = lane >> 3, chunk = lane & 7;
-        const bool all_fast = a.vec && rows == 32 && col0 + 128 <= (int64_t)a.k;
-        if (all_fast) {   // all loads first: rows 4 i + sub, columns 32 g + 4 chunk on
-#pragma unroll
-          for (int g = 0; g < 4; ++g)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 v = load4<OUT_BF16>(a.grad, r0 * a.gs + col0 + g * 32 + (4 * i + sub) * a.gs + chunk * 4);
-              sum[g * 32 + i * 4] = v.x;
-              sum[g * 32 + i * 4 + 1] = v.y;
-              sum[g * 32 + i * 4 + 2] = v.z;
-              sum[g * 32 + i * 4 + 3] = v.w;
-            }
-        }
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          int cols;
-          bool fast;
-          const int64_t at = block(g, cols, fast);
-          __syncwarp();
-          if (all_fast) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              stg[(4 * i + sub) * 8 + (chunk ^ ((4 * i + sub) & 7))] =
-                  make_float4(sum[g * 32 + i * 4], sum[g * 32 + i * 4 + 1], sum[g * 32 + i * 4 + 2], sum[g * 32 + i * 4 + 3]);
-          } else {
-            block_in_any<OUT_BF16>(a, at, rows, cols, lane, stg);
-          }
-          __syncwarp();
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const float4 v = stg[lane * 8 + (c ^ (lane & 7))];
-            sum[g * 32 + c * 4] = v.x;
-            sum[g * 32 + c * 4 + 1] = v.y;
-            sum[g * 32 + c * 4 + 2] = v.z;
-            sum[g * 32 + c * 4 + 3] = v.w;
-          }
-        }
-      }
       for (uint32_t c0 = w.s0; c0 < w.s1; c0 += kChunk) {
         if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, wait_ns))) {
           timed_out = true;
@@ -397,6 +371,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) red_release_gpu_add(a.ready + w.left_tile * 16 + me, 1);
         continue;
       }
+      // The old gradient is added last, once: to it, chunks of the sum that are each below half its
+      // step would be lost one by one. It is read one block ahead of its use.
+      float4 old[8];
+      auto fetch_old = [&](int g) {
+        int cols;
+        bool fast;
+        const int64_t at = block(g, cols, fast);
+        if (a.accumulate && fast) block_load<OUT_BF16>(a, at, lane, old);
+      };
+      fetch_old(0);
       if (w.others) {
         // the last unit of the pair: the operand ring is free, and brings the parts in pieces of
         // 64 columns, kJoin of them ahead
@@ -449,7 +433,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           stg[lane * 8 + (c ^ (lane & 7))] = make_float4(sum[g * 32 + c * 4], sum[g * 32 + c * 4 + 1],
                                                          sum[g * 32 + c * 4 + 2], sum[g * 32 + c * 4 + 3]);
         __syncwarp();
-        block_out<OUT_BF16>(a, at, rows, cols, fast, lane, stg);
+        if (fast) {
+          float4 v[8];
+          block_sums(lane, stg, a.accumulate, old, v);
+          if (g < 3) fetch_old(g + 1);
+          block_store<OUT_BF16>(a, at, lane, v);
+        } else {
+          block_out_any<OUT_BF16>(a, at, rows, cols, lane, stg);
+        }
       }
     }
     if (timed_out && lane == 0) raise_abort(abort_flag, true, rank);

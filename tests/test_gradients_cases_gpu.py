@@ -1,0 +1,29 @@
+"""The gradient-making operators on calls with a history or a size of their own.
+
+Tolerances as in test_gradients_gpu: roundings counted element by element."""
+import pytest
+import torch
+
+from .test_gradients_gpu import BF16, DTS, FP32, Guarded
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------- weight gradient
+
+@pytest.mark.parametrize("dy_dt", DTS)
+@pytest.mark.parametrize("rows,n,k", [(16384, 256, 256), (16384, 100, 333), (16384, 512, 9472), (700, 512, 9472)])
+def test_weight_grad_onto_a_large_gradient(rows, n, k, dy_dt):
+    """Sums whose parts are each below half a step of the old gradient, but not the whole: the old
+    value enters once. Every sum is a multiple of 2^-36 (2^-33 for 700 rows) below 2^24 of them, so
+    exact, and so is 1 + 2^-22; 700 rows: their sum is 0.68 of the step above 1, and rounds to it."""
+    import newton_schulz_13_b200 as ns
+    ck = ns.checkpoint_store(torch.ones(rows, k, dtype=BF16, device="cuda"))
+    unit, want = (2.0 ** -36, 1 + 2.0 ** -22) if rows == 16384 else (2.0 ** -33, 1 + 2.0 ** -23)
+    dy = torch.full((rows, n), unit, dtype=dy_dt, device="cuda")
+    for extra in (0, 1):
+        out = Guarded(n, k, FP32, extra, extra, fill=1.0)
+        got = ns.weight_grad(dy, ck, grad=out.view, accumulate=True)
+        assert torch.equal(got, torch.full((n, k), want, device="cuda")), got.double().sub(1).abs().max().item()
+        out.check()
+    assert ns.check_status() == ns.OK
