@@ -311,11 +311,12 @@ MUON_API int muon_weight_grad(const void* dy, muon_dtype_t dy_dtype, int64_t dy_
  * stays valid until the next call on that thread. */
 MUON_API const char* muon_last_error(void);
 
-/* Synchronises `stream`, then reads and clears the device status word of the current device.
- * Returns MUON_ERR_TIMEOUT if a kernel gave up waiting since the last check,
- * MUON_WARN_TOKEN if an embedding call met a token id past the vocabulary, MUON_WARN_NONFINITE if
- * a NaN or Inf reached an update matrix, MUON_OK otherwise (the first that applies; all are cleared)
- * (or MUON_ERR_CUDA if synchronising failed). */
+/* Synchronises `stream`, then reads the device status of the current device and clears what it
+ * returns: MUON_ERR_TIMEOUT if a kernel gave up waiting since the last check (which clears a NaN's
+ * record too), MUON_WARN_NONFINITE if a NaN or Inf reached an update matrix, MUON_WARN_TOKEN if an
+ * embedding call met a token id past the vocabulary, MUON_OK otherwise. The first that applies; a
+ * token's warning that had to give way comes with the next call. MUON_ERR_CUDA if synchronising
+ * failed. */
 MUON_API int muon_check_status(muon_stream_t stream);
 
 /* Frees the workspace and cached plans of the current device (synchronises the device). */

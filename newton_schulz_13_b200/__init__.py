@@ -226,7 +226,8 @@ def adamw_step(params: List, grads: List, exp_avg: List, exp_avg_sq: List, step:
 
 
 def check_status(stream=None) -> int:
-    """Synchronises the stream and returns OK, WARN_NONFINITE or WARN_TOKEN; raises on a device timeout."""
+    """Synchronises the stream and returns OK, WARN_NONFINITE or WARN_TOKEN; raises on a device timeout.
+    What it reports is cleared; a token's warning gives way to the others and comes with the next call."""
     return _check(lib.muon_check_status(_stream_handle(stream)))
 
 

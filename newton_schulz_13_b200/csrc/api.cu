@@ -230,7 +230,7 @@ struct DeviceState {
   char* arena = nullptr;                      // per-wave buffers shared by every plan
   size_t arena_bytes = 0;
   uint64_t arena_gen = 0;                     // bumped whenever the arena moves
-  int* d_status = nullptr;  // [0] flags, [1] non-finite count
+  int* d_status = nullptr;  // kStatusWords words (muon_internal.h)
   int sms = 0;
   int cc_major = 0;
   int pair_capacity = 0;   // resident CTA pairs of the paired tensor-core kernel
@@ -255,8 +255,8 @@ int device_state(DeviceState** out) {
   if (ds.pair_capacity == 0) ds.pair_capacity = gemm_tc_pair_capacity(ds.sms);
   if (ds.x3_capacity == 0) ds.x3_capacity = gemm_x3_pair_capacity(ds.sms);
   if (!ds.d_status) {
-    MUON_CUDA(cudaMalloc(&ds.d_status, 2 * sizeof(int)));
-    MUON_CUDA(cudaMemset(ds.d_status, 0, 2 * sizeof(int)));
+    MUON_CUDA(cudaMalloc(&ds.d_status, kStatusWords * sizeof(int)));
+    MUON_CUDA(cudaMemset(ds.d_status, 0, kStatusWords * sizeof(int)));
   }
   *out = &ds;
   return MUON_OK;
@@ -1091,12 +1091,19 @@ int muon_check_status(muon_stream_t stream) {
   int rc = device_state(&ds);
   if (rc != MUON_OK) return rc;
   MUON_CUDA(cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)));
-  int h[2] = {0, 0};
+  int h[kStatusWords] = {};
   MUON_CUDA(cudaMemcpy(h, ds->d_status, sizeof(h), cudaMemcpyDeviceToHost));
-  MUON_CUDA(cudaMemset(ds->d_status, 0, sizeof(h)));
-  if (h[0] & kStatusTimeout) return fail(MUON_ERR_TIMEOUT, "a kernel wait hit its time limit");
-  if (h[0] & kStatusToken) return fail(MUON_WARN_TOKEN, "a token id was past the vocabulary");
-  if (h[1] != 0) return fail(MUON_WARN_NONFINITE, std::to_string(h[1]) + " chunk(s) held NaN or Inf");
+  // a token id past the vocabulary is harmless (a zero row), so its report gives way to the others
+  // and waits for the next call; a time limit that ran out makes the non-finite count meaningless
+  if (h[0] & kStatusTimeout || h[kStatusNonfinite] != 0) {
+    MUON_CUDA(cudaMemset(ds->d_status, 0, kStatusToken * sizeof(int)));
+    if (h[0] & kStatusTimeout) return fail(MUON_ERR_TIMEOUT, "a kernel wait hit its time limit");
+    return fail(MUON_WARN_NONFINITE, std::to_string(h[kStatusNonfinite]) + " chunk(s) held NaN or Inf");
+  }
+  if (h[kStatusToken] != 0) {
+    MUON_CUDA(cudaMemset(ds->d_status + kStatusToken, 0, sizeof(int)));
+    return fail(MUON_WARN_TOKEN, "a token id was past the vocabulary");
+  }
   return MUON_OK;
 }
 

@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kEwThreads, 4) prologue_kernel(const MatInfo* 
     }
     const float total = block_sum(sq, red);
     if (threadIdx.x == 0) partials[chunk] = total;
-    if (bad) atomicAdd(status + 1, 1);
+    if (bad) atomicAdd(status + kStatusNonfinite, 1);
   }
 }
 

@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(EmbedArgs a) {
   const int64_t id = load_id<ID64>(a.tokens, row);
   const int64_t c0 = ((int64_t)blockIdx.y * kPart * 32 + lane) * V;
   const bool have = id >= 0 && id < a.vocab;
-  if (id >= a.vocab && c0 == 0) atomicOr(a.status, kStatusToken);
+  if (id >= a.vocab && c0 == 0) atomicOr(a.status + kStatusToken, 1);
   Raw<V, T_BF16> raw[kPart];
 #pragma unroll
   for (int j = 0; j < kPart; ++j)
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) token_sort_kernel(EmbedGradAr
       __syncwarp();
     }
   }
-  if (me == 0 && bad) atomicOr(a.status, kStatusToken);
+  if (me == 0 && bad) atomicOr(a.status + kStatusToken, 1);
   below = __reduce_add_sync(0xffffffffu, below);
   if (lane == 0) warp_part[warp] = below;
   __syncthreads();

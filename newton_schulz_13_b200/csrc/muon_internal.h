@@ -17,9 +17,10 @@ constexpr int kEwThreads = 256;
 constexpr int kCsRows = 64;
 constexpr int kCsCols = 256;
 
-// Device status word bits.
-constexpr int kStatusTimeout = 1;
-constexpr int kStatusToken = 2;   // a token id past the vocabulary (embedding, embedding gradient)
+// Device status words: [0] bits, [1] chunks that held a NaN or an infinity, [2] nonzero after a token
+// id past the vocabulary (embedding, embedding gradient). Each is cleared when it has been reported.
+constexpr int kStatusTimeout = 1;   // bit of word 0
+constexpr int kStatusNonfinite = 1, kStatusToken = 2, kStatusWords = 3;   // words
 
 // Per-matrix record read by the elementwise kernels.
 struct MatInfo {

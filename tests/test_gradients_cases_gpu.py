@@ -4,7 +4,7 @@ Tolerances as in test_gradients_gpu: roundings counted element by element."""
 import pytest
 import torch
 
-from .test_gradients_gpu import BF16, DTS, FP32, Guarded
+from .test_gradients_gpu import BF16, DTS, FP32, Guarded, normal
 
 pytestmark = pytest.mark.gpu
 
@@ -26,4 +26,46 @@ def test_weight_grad_onto_a_large_gradient(rows, n, k, dy_dt):
         got = ns.weight_grad(dy, ck, grad=out.view, accumulate=True)
         assert torch.equal(got, torch.full((n, k), want, device="cuda")), got.double().sub(1).abs().max().item()
         out.check()
+    assert ns.check_status() == ns.OK
+
+
+# ---------------------------------------------------------------------------- status
+
+def test_a_token_warning_hides_no_other():
+    """A batch with an id past the vocabulary and a NaN in an update matrix: both are reported, the
+    graver first, whichever came first; and a time limit that ran out does not take the warning along."""
+    import newton_schulz_13_b200 as ns
+    table = normal((10, 64), FP32, 163)
+    past = torch.tensor([3, 10], device="cuda")
+
+    def token(grad):
+        if grad:
+            ns.embedding_grad(past, normal((2, 64), FP32, 164), 10)
+        else:
+            ns.embedding(past, table)
+
+    def nan():
+        g = normal((64, 64), FP32, 165)
+        g[3, 4] = float("nan")
+        ns.muon_step([normal((64, 64), FP32, 166)], [g], [torch.zeros(64, 64, device="cuda")], lr=0.02)
+
+    assert ns.check_status() == ns.OK
+    for grad in (False, True):
+        for order in (0, 1):
+            for call in ((lambda: token(grad)), nan) if order else (nan, (lambda: token(grad))):
+                call()
+            assert ns.check_status() == ns.WARN_NONFINITE
+            assert ns.check_status() == ns.WARN_TOKEN
+            assert ns.check_status() == ns.OK
+    dy, ck = normal((4096, 1024), BF16, 167), ns.checkpoint_store(normal((4096, 1024), BF16, 168))
+    token(False)
+    ns.set_wait_limit_ns(1)
+    try:
+        ns.weight_grad(dy, ck)
+        with pytest.raises(ns.MuonError) as e:
+            ns.check_status()
+        assert e.value.code == ns.ERR_TIMEOUT
+    finally:
+        ns.set_wait_limit_ns(0)
+    assert ns.check_status() == ns.WARN_TOKEN
     assert ns.check_status() == ns.OK
