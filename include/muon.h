@@ -257,7 +257,8 @@ MUON_API int muon_embedding_grad(const void* tokens, int token_bits, int64_t n, 
  *   y[t] = h[t] rstd[t] weight
  *   codes, scales: the checkpoint of y before its rounding (see muon_checkpoint_store)
  * y (x's type) or codes and scales may be NULL, not all of them. h may be the residual or x, and y
- * may be x, where pointer, stride and type are the same.
+ * may be x, where pointer, stride and type are the same (without a residual, y over x leaves no h
+ * for the gradient).
  */
 MUON_API int muon_rms_norm(const void* x, muon_dtype_t x_dtype, int64_t x_stride, const void* residual,
                            muon_dtype_t r_dtype, int64_t r_stride, const void* weight, muon_dtype_t w_dtype,

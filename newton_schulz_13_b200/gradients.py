@@ -81,7 +81,7 @@ class ActCheckpoint(NamedTuple):
 
 class RmsNorm(NamedTuple):
     y: Optional[torch.Tensor]
-    h: torch.Tensor
+    h: Optional[torch.Tensor]
     rstd: torch.Tensor
     checkpoint: Optional[ActCheckpoint]
 
@@ -278,7 +278,7 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-5, output: bool = True, c
     """h = x + residual (in the residual's type; x itself without one), y = h / rms(h) * weight in
     x's type, rstd = 1 / rms(h) per row (fp32), and with checkpoint=True an ActCheckpoint of y.
     output=False leaves y out (y None). `h` and `y` may be given as buffers: h may be the residual
-    or, in its type, x; y may be x."""
+    or, in its type, x; y may be x, and where there is no residual no h is left then (h None)."""
     if h is None and y is None and stream is None and _fast is not None:
         got = _fast.rms_norm(x, weight, residual, eps, output, checkpoint)
         if got is not None:
@@ -329,7 +329,9 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-5, output: bool = True, c
         qp, sp, ss = ck[0].data_ptr(), ck[1].data_ptr(), -(-dim // MX_BLOCK)
     _check(lib.muon_rms_norm(x.data_ptr(), xc, xs, rp, rc, rs, weight.data_ptr(), wc, x.numel() // dim if dim else 0, dim, eps,
                              hp, hs, yp, ys, qp, dim, sp, ss, rstd.data_ptr(), _stream(dev)))
-    return RmsNorm(y, x if h is None else h, rstd, ck)
+    if residual is None and (y is None or y.data_ptr() != x.data_ptr() or not x.numel()):
+        h = x
+    return RmsNorm(y, h, rstd, ck)
 
 
 def rms_norm_grad(dy, h, weight, rstd, dh=None, dx=None, dweight=None, accumulate: bool = False, stream=None):

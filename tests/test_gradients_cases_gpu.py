@@ -69,3 +69,27 @@ def test_a_token_warning_hides_no_other():
         ns.set_wait_limit_ns(0)
     assert ns.check_status() == ns.WARN_TOKEN
     assert ns.check_status() == ns.OK
+
+
+# ---------------------------------------------------------------------------- RMS norm
+
+def test_rms_norm_output_over_the_input():
+    """Where y takes x's place and there is no residual, no h remains to be returned."""
+    import newton_schulz_13_b200 as ns
+    for shape in ((3, 5, 64), (1100, 4096), (9, 77)):
+        x, w = normal(shape, BF16, 173), normal(shape[-1:], FP32, 174)
+        want = ns.rms_norm(x, w)
+        assert want.h is x
+        for alias in (lambda b: b, lambda b: b.view(shape), lambda b: b.detach()):
+            buf = x.clone()
+            got = ns.rms_norm(buf, w, y=alias(buf))
+            assert torch.equal(got.y, want.y) and torch.equal(got.rstd, want.rstd)
+            assert got.h is None
+        other = torch.empty_like(x)
+        assert ns.rms_norm(x, w, y=other).h is x and torch.equal(other, want.y)
+        buf, res = x.clone(), normal(shape, FP32, 175)
+        got, ref = ns.rms_norm(buf, w, residual=res, y=buf), ns.rms_norm(x, w, residual=res)
+        assert torch.equal(got.h, ref.h) and torch.equal(buf, ref.y)
+    x = torch.empty(0, 64, device="cuda")
+    assert ns.rms_norm(x, torch.ones(64, device="cuda"), y=torch.empty(0, 64, device="cuda")).h is x      # nothing overwritten
+    assert ns.check_status() == ns.OK
