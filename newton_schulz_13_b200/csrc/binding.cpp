@@ -84,6 +84,13 @@ bool number(PyObject* o, double* v) {
   return true;
 }
 
+// A truth value; -1 if it has none (the full path then meets the error again and raises it).
+int truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) PyErr_Clear();
+  return v;
+}
+
 int token_bits(const Tensor& t) { return t.scalar_type() == ScalarType::Long ? 64 : t.scalar_type() == ScalarType::Int ? 32 : 0; }
 
 #define NONE_IF(cond) \
@@ -131,7 +138,7 @@ PyObject* embedding_grad(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     return none();
   }
   NONE_IF(d->sizes().slice(0, d->dim() - 1) != t->sizes() || vocab < 1);
-  const int bits = token_bits(*t), dc = code(d->scalar_type()), acc = PyObject_IsTrue(args[6]);
+  const int bits = token_bits(*t), dc = code(d->scalar_type()), acc = truth(args[6]);
   NONE_IF(!bits || dc < 0 || acc < 0);
   Tensor grad;
   if (args[4] == Py_None) {
@@ -163,8 +170,8 @@ PyObject* rms_norm(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   double eps;
   NONE_IF(!x || !w || !number(args[3], &eps));
   const int64_t dim = x->sizes().back(), blocks = (dim + 31) / 32;
-  const int xc = code(x->scalar_type()), wc = code(w->scalar_type()), output = PyObject_IsTrue(args[4]),
-            checkpoint = PyObject_IsTrue(args[5]);
+  const int xc = code(x->scalar_type()), wc = code(w->scalar_type()), output = truth(args[4]),
+            checkpoint = truth(args[5]);
   NONE_IF(xc < 0 || wc < 0 || w->dim() != 1 || w->size(0) != dim || dim < 1 || output < 0 || checkpoint < 0 || (!output && !checkpoint));
   const Tensor* r = nullptr;
   Tensor h, y, q, s;
@@ -282,7 +289,7 @@ PyObject* weight_grad(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   const Tensor *d = plain(args[0], c.dev), *q, *s;
   NONE_IF(!d || !checkpoint_of(args[1], args[2], c.dev, &q, &s));
   const int64_t n = d->sizes().back(), k = q->sizes().back();
-  const int dc = code(d->scalar_type()), acc = PyObject_IsTrue(args[5]);
+  const int dc = code(d->scalar_type()), acc = truth(args[5]);
   NONE_IF(dc < 0 || n < 1 || acc < 0 || d->dim() != q->dim() || d->sizes().slice(0, d->dim() - 1) != q->sizes().slice(0, q->dim() - 1));
   Tensor grad;
   if (args[3] == Py_None) {

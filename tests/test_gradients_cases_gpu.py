@@ -93,3 +93,31 @@ def test_rms_norm_output_over_the_input():
     x = torch.empty(0, 64, device="cuda")
     assert ns.rms_norm(x, torch.ones(64, device="cuda"), y=torch.empty(0, 64, device="cuda")).h is x      # nothing overwritten
     assert ns.check_status() == ns.OK
+
+
+# ---------------------------------------------------------------------------- arguments
+
+@pytest.mark.parametrize("plain", [True, False])
+def test_arguments_without_a_truth_value(plain, monkeypatch):
+    """An argument whose truth value cannot be had raises its own error."""
+    import newton_schulz_13_b200 as ns
+    ns.ActCheckpoint
+    from newton_schulz_13_b200 import gradients
+    if not plain:
+        monkeypatch.setattr(gradients, "_fast", None)
+
+    class Unsure:
+        def __bool__(self):
+            raise ZeroDivisionError("unsure")
+
+        __int__ = __index__ = __bool__
+
+    x, w = normal((4, 64), BF16, 169), torch.ones(64, device="cuda")
+    t = torch.arange(4, device="cuda")
+    grad, ck = torch.zeros(64, 64, device="cuda"), ns.checkpoint_store(x)
+    for call in (lambda: ns.rms_norm(x, w, output=Unsure()), lambda: ns.rms_norm(x, w, checkpoint=Unsure()),
+                 lambda: ns.embedding_grad(t, x, 64, grad=grad, accumulate=Unsure()),
+                 lambda: ns.weight_grad(x, ck, grad=grad, accumulate=Unsure())):
+        with pytest.raises(ZeroDivisionError):
+            call()
+    assert ns.check_status() == ns.OK
