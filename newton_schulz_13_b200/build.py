@@ -1,4 +1,4 @@
-"""Builds, in-tree, libmuon.so (the sm_100a kernels and the C ABI) with nvcc, and _plain.so (the plain
+"""Builds, in-tree, libmuon.so (the sm_100a kernels and the C ABI) with nvcc, and _plain.*.so (the plain
 case of the gradient operators' Python calls, csrc/binding.cpp) with g++."""
 from __future__ import annotations
 
@@ -50,26 +50,35 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     return LIB
 
 
-BINDING = os.path.join(HERE, "_plain.so")
+def binding_path() -> str:
+    """Where the extension lies that was built for this interpreter and this torch, whose layouts it
+    holds: one that was built for others has another name."""
+    import sysconfig
+
+    import torch
+    version = f"{torch.__version__}-{str(torch.version.git_version)[:8]}-{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    return os.path.join(HERE, f"_plain.{sysconfig.get_config_var('SOABI')}.torch-{version}.so")
 
 
 def binding_stale() -> bool:
-    if not os.path.exists(BINDING):
+    path = binding_path()
+    if not os.path.exists(path):
         return True
-    t = os.path.getmtime(BINDING)
+    t = os.path.getmtime(path)
     return any(os.path.getmtime(d) > t for d in (os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "muon.h")))
 
 
 def build_binding(force: bool = False, verbose: bool = False) -> str:
+    path = binding_path()
     if not force and not binding_stale():
-        return BINDING
+        return path
     import sysconfig
 
     import torch
     home = os.path.dirname(torch.__file__)
     inc, libs = os.path.join(home, "include"), os.path.join(home, "lib")
     cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
-    out = f"{BINDING}.{os.getpid()}"
+    out = f"{path}.{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-Wno-attributes",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
@@ -78,8 +87,8 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.check_call(cmd)
-    os.replace(out, BINDING)
-    return BINDING
+    os.replace(out, path)
+    return path
 
 
 if __name__ == "__main__":

@@ -9,7 +9,7 @@ the root-mean-square norm, and 8-bit activation checkpoints with the weight grad
 
 Argument marshalling only, as in the rest of the package; include/muon.h has the formulas. The plain
 case of a call (contiguous tensors of the current device, outputs to be allocated, the current
-stream) goes through _plain.so (csrc/binding.cpp): 4-7 us of the interpreter's time instead of 10-23.
+stream) goes through the extension _plain (csrc/binding.cpp): 4-7 us of the interpreter's time instead of 10-23.
 Any other, and any that is refused, takes the path below through ctypes. Inputs
 are CUDA tensors whose last dimension is contiguous (rows may be strided); leading dimensions are
 taken as rows. Outputs and workspaces come from torch's allocator on the stream the call runs on
@@ -20,6 +20,8 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import warnings
 from typing import NamedTuple, Optional
 
@@ -49,15 +51,16 @@ for _name, _args in {"muon_embedding_grad_workspace": [_i64, _i64, _i64], "muon_
 
 
 def _load_plain():
-    """The extension, built if it is missing or older than its source; None where that fails: every
-    call then takes the path through ctypes, to the same kernels."""
+    """The extension, built if there is none for this interpreter and torch or it is older than its
+    source; None where that fails: every call then takes the path through ctypes, to the same kernels."""
     from . import build as _build
     try:
-        if _build.binding_stale():
-            _build.build_binding()
-        from . import _plain
+        name, path = __package__ + "._plain", _build.build_binding()
+        loader = importlib.machinery.ExtensionFileLoader(name, path)
+        _plain = importlib.util.module_from_spec(importlib.util.spec_from_file_location(name, path, loader=loader))
+        loader.exec_module(_plain)
     except Exception as e:  # noqa: BLE001
-        warnings.warn(f"{_build.BINDING} is not usable ({e}); calls go through ctypes")
+        warnings.warn(f"the extension of the plain calls is not usable ({e}); calls go through ctypes")
         return None
     _plain.bind(*(ctypes.cast(getattr(lib, "muon_" + n), _vp).value for n in (
         "embedding", "embedding_grad", "embedding_grad_workspace", "rms_norm", "rms_norm_grad", "rms_norm_grad_workspace",
