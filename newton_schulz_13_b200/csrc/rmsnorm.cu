@@ -615,6 +615,22 @@ cudaError_t norm_grad_shapes(const NormGradArgs& a, bool v8, int* blocks, cudaSt
   return norm_grad_one<1, 32, D, H, Feed::kDirect, 1>(a, row_shape(a.dim, 32, 256), 0, 1, blocks, st);
 }
 
+// Whether many rows go through the ring (us with residual, y and checkpoint unless said otherwise, ring
+// and not, of 2^24 elements in all; below 2^22 starting it costs up to 1 us more: 64 x 4096 bf16 3.6
+// and 2.9):
+//   unaligned rows: yes (31 columns 186 and 339, 257 113 and 124, 4093 76 and 128)
+//   bf16: from 2304 columns on (2304 45 and 45, 4096 31 and 37, 8192 31 and 41), and below where the
+//     row leaves no more than a quarter of its threads' accesses idle (1024 33 and 35, 768 40 and 39,
+//     but 1280 46 and 43, 256 38 and 30, 128 72 and 47)
+//   an fp32 tensor in it: from 4104 columns on (5120, residual fp32: 43 and 54; x fp32, no residual: 43
+//     and 45), below no (4096, residual fp32: 45 and 42; 1024, x fp32, no residual: 33 and 31)
+//   two: no (8192 57 and 51, 1024 57 and 50)
+bool ring_pays(const NormArgs& a, bool v8, int x_bf16, int r_bf16) {
+  if (!v8) return true;
+  if (x_bf16 && r_bf16) return a.dim > 2048 || a.dim / 8 * 4 >= 3 * 2 * row_shape(a.dim / 8, 2, 512).tpr;
+  return a.dim > 4096 && (!a.r || x_bf16 || r_bf16);
+}
+
 int norm_grad_blocks(int64_t rows) {
   const int64_t cap = (int64_t)kSms * 2;   // two blocks per SM at most
   return (int)(rows < cap ? rows : cap);
@@ -628,10 +644,7 @@ cudaError_t launch_rms_norm(const NormArgs& a, int x_bf16, int r_bf16, int sms, 
                   (!a.r || (aligned8(a.r, a.rs, r_bf16) && aligned8(a.h, a.hs, r_bf16))) &&
                   (!a.y || aligned8(a.y, a.ys, x_bf16)) &&
                   (!a.q || ((uintptr_t)a.q % 8 == 0 && a.qs % 8 == 0));
-  // from 2^22 elements on the ring is no slower (us, bf16 with residual, y and checkpoint, ring and
-  // not: 1024 x 4096 10.0 and 9.9, 4096 x 4096 27 and 32, 16384 x 4096 93 and 112, 1024 x 8192 15 and
-  // 19); below, starting it costs up to 1 us more (64 x 4096 3.6 and 2.9)
-  if (a.dim <= 8192 && a.rows * a.dim >= (int64_t(1) << 22)) {
+  if (a.dim <= 8192 && a.rows * a.dim >= (int64_t(1) << 22) && ring_pays(a, v8, x_bf16, r_bf16)) {
     if (v8) {
       if (x_bf16) return r_bf16 ? norm_ring<8, true, true>(a, st) : norm_ring<8, true, false>(a, st);
       return r_bf16 ? norm_ring<8, false, true>(a, st) : norm_ring<8, false, false>(a, st);

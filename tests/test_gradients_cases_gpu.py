@@ -181,6 +181,28 @@ def test_rms_norm_many_unaligned_rows(rows, dim, x_dt, r_dt):
     assert ns.check_status() == ns.OK
 
 
+@pytest.mark.parametrize("x_dt,r_dt", PAIRS)
+@pytest.mark.parametrize("rows,dim", [(11000, 384), (8200, 512), (9000, 520), (2100, 2048), (1900, 2304), (1030, 4104), (900, 5120),
+                                      (600, 8192)])
+def test_rms_norm_many_aligned_rows(rows, dim, x_dt, r_dt):
+    """On both sides of every bound of the choice between the ring and the threads' own loads."""
+    import newton_schulz_13_b200 as ns
+    x, r = normal((rows, dim), x_dt, 190), None if r_dt is None else normal((rows, dim), r_dt, 191, 2.0)
+    w = 1.0 + 0.1 * torch.randn(dim, generator=gen(192), device="cuda")
+    got = ns.rms_norm(x, w, residual=r, eps=1e-5, checkpoint=True)
+    want_h, want_rstd, want = norm_want(x, r, w, 1e-5)
+    assert torch.equal(got.h, want_h)
+    within(got.rstd, want_rstd, want_rstd * SUM * E, "rstd")
+    within(got.y, want, want.abs() * (SUM * E + U[x_dt]), "y")
+    each = got.checkpoint.scales.double().repeat_interleave(32, 1)[:, :dim]
+    within(ns.checkpoint_restore(got.checkpoint, dtype=FP32), want, want.abs() * (2.0 ** -4 + SUM * E) + each * 2.0 ** -10, "checkpoint")
+    xi, ri = x.clone(), None if r is None else r.clone()
+    same = ns.rms_norm(xi, w, residual=ri, h=ri, y=xi, checkpoint=True)
+    assert torch.equal(xi, got.y) and (r is None or torch.equal(ri, got.h))
+    assert torch.equal(same.checkpoint.q.view(torch.uint8), got.checkpoint.q.view(torch.uint8))
+    assert ns.check_status() == ns.OK
+
+
 @pytest.mark.parametrize("dy_dt", DTS)
 @pytest.mark.parametrize("h_dt", DTS)
 @pytest.mark.parametrize("rows,dim", [(20000, 72), (20000, 71), (6000, 1024), (6000, 1023), (3000, 4096), (3000, 4093), (1500, 8192),
