@@ -78,9 +78,4 @@ __device__ __forceinline__ float2 mx_unpack2(uint32_t codes) {
   return __half22float2(__half2(h));
 }
 
-__device__ __forceinline__ float mx_unpack1(uint32_t code) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)(code & 0xffu), __NV_E4M3);
-  return __half2float(__half(h));
-}
-
 }  // namespace muon
