@@ -237,10 +237,11 @@ MUON_API int muon_embedding(const void* tokens, int token_bits, int64_t n, const
 /*
  * Its gradient by the table, from sorted tokens:
  *   grad[v][:] = (accumulate ? grad[v][:] : 0) + scale * sum over t with id_t = v of dy[t][:]
- * summed in fp32 and rounded once, in an order that goes by the places t alone (an id's first 8
- * places in their order, the next 8, and so on; then these sums by eights). Without accumulate every row of grad is
- * written (zeros for absent tokens); with it, the rows of absent tokens are not touched. Ids
- * outside [0, vocab) contribute nothing (ids >= vocab are reported as above).
+ * summed in fp32 and rounded once, in an order that goes by the places t alone (an id's places in
+ * their order; from 16 of them on, sums of 8 places each, the last one of up to 15, then of these
+ * sums by eights). Without accumulate every row of grad is written (zeros for absent tokens); with
+ * it, the rows of absent tokens are not touched. Ids outside [0, vocab) contribute nothing (ids >=
+ * vocab are reported as above).
  */
 MUON_API int64_t muon_embedding_grad_workspace(int64_t n, int64_t vocab, int64_t dim);
 MUON_API int muon_embedding_grad(const void* tokens, int token_bits, int64_t n, const void* dy, muon_dtype_t dy_dtype,
@@ -299,8 +300,10 @@ MUON_API int muon_checkpoint_restore(const void* codes, int64_t codes_stride, co
 /*
  * Weight gradient of y = x W^T from dy and the checkpoint of x:
  *   grad[i][j] = (accumulate ? grad[i][j] : 0) + sum over t of dy[t][i] x[t][j],  i < n, j < k
- * on the tensor cores. An fp32 dy enters as three bf16 terms that sum to it exactly. rows <= 2^29,
- * n and k <= 2^20; rows = 0 gives zeros (or leaves grad, accumulating).
+ * on the tensor cores. An fp32 dy enters as three bf16 terms that sum to it: exactly from 2^-110 on,
+ * and short by less than 2^-133 (bf16's smallest number) below. The old grad is added once, to the
+ * whole sum. rows <= 2^29, n and k <= 2^20; rows = 0 gives zeros (or leaves grad, accumulating). The
+ * workspace has room for a copy of dy, which a bf16 dy with 16-byte aligned rows does not need.
  */
 MUON_API int64_t muon_weight_grad_workspace(int64_t rows, int64_t n, int64_t k, muon_dtype_t dy_dtype);
 MUON_API int muon_weight_grad(const void* dy, muon_dtype_t dy_dtype, int64_t dy_stride, const void* codes,

@@ -1,12 +1,14 @@
 // Weight gradient from an 8-bit activation checkpoint: grad[n][k] (+)= sum over t of dy[t][n] x[t][k],
 // with x the checkpoint's values (mx.cuh), which are exact in bf16. Compute-bound: 2 rows n k FLOPs
-// on the tcgen05 tensor cores. 14336 x 4096 over 8192 rows: 664 us with the staging (1450 TFLOP/s, the
-// tensor pipe busy 88 % of the time); 768 x 2304, accumulating in fp32: 50 us.
+// on the tcgen05 tensor cores. 14336 x 4096 over 8192 rows: 664 us with the staging in short runs (1450
+// TFLOP/s, the tensor pipe busy 88 % of the time), 780 to 810 over seconds under the power limit; 768 x
+// 2304, accumulating in fp32: 47 us, 92 from an fp32 dy.
 //
 // Two launches:
 //   stage    x (and dy, when its rows are not 16-byte aligned or it is fp32) written to the
-//            workspace as bf16. An fp32 dy becomes three bf16 planes whose sum is dy exactly
-//            (8 + 8 + 8 mantissa bits, by truncation), so nothing of it is lost.
+//            workspace as bf16. An fp32 dy becomes three bf16 planes whose sum is dy (8 + 8 + 8
+//            mantissa bits, by truncation): exactly from 2^-110 on; below, the third plane
+//            ends at bf16's smallest number, 2^-133, and what is under it is cut off.
 //   product  CTA pairs (cta_group::2) on 256 x 256 tiles; both operands are MN-major (the
 //            contraction runs over rows t). Warp 0 loads 64-row slices with TMA (one of x, one of
 //            each plane of dy), warp 1 of the even CTA issues the MMAs, eight warps drain the
@@ -16,7 +18,7 @@
 //            Whole tiles go to the pairs in rounds; the slices of the tiles left over after the
 //            last full round are dealt out evenly. Where a tile so falls to several pairs, the one
 //            with its last slices adds the others' sums, which come through the workspace in fp32,
-//            to its own, always in the same order. It waits only for pairs of lower numbers, whose
+//            to its own, always in the same order. The old gradient is added last. It waits only for pairs of lower numbers, whose
 //            blocks start no later than its own, and for work that they do first.
 // Waits are bounded as in the Newton-Schulz products (pair_pipe.cuh describes the unwinding).
 #include <cuda.h>

@@ -52,6 +52,19 @@ def test_weight_grad_more_tiles_than_pairs(rows, n, k, dy_dt, acc):
     assert ns.check_status() == ns.OK
 
 
+@pytest.mark.parametrize("e", [-100, -110, -111, -120, -126, -140, -149])
+def test_weight_grad_of_small_fp32_values(e):
+    """Three truncated terms of 8 bits hold a number from 2^-110 on; below, the third ends at 2^-133,
+    bf16's smallest number. One row, so that nothing else is rounded (2^20 keeps the products normal)."""
+    import newton_schulz_13_b200 as ns
+    ck = ns.checkpoint_store(torch.full((1, 32), 2.0 ** 20, device="cuda"))
+    m = torch.randint(1 << 23, 2 << 23, (1, 512), generator=gen(193), device="cuda").double()
+    dy = (m * 2.0 ** (e - 23) * torch.where(m % 2 == 0, 1.0, -1.0)).float()
+    got = ns.weight_grad(dy, ck).double() * 2.0 ** -20
+    off = (got - dy.double().t()).abs().max().item()
+    assert off == 0.0 if e >= -110 else off < 2.0 ** -133
+
+
 # ---------------------------------------------------------------------------- status
 
 def test_a_token_warning_hides_no_other():
