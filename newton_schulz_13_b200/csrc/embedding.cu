@@ -16,7 +16,7 @@
 //           become one again, up to the run's. Between these blocks lie others that zero the rows
 //           of absent ids: most of the bytes where the vocabulary is large.
 // 16384 tokens into 128256 x 4096 bf16: 14 + 190 us (5.9 TB/s); 12276 into 50257 x 768 fp32: 12 + 16 us,
-// bound by latency.
+// bound by the sort's two serial walks over a warp's tokens and the levels of the joining.
 #include <cuda_bf16.h>
 #include <stdint.h>
 

@@ -7,8 +7,11 @@
 // reads back, and the checkpoint of the unrounded y, so each of its values is rounded once.
 //
 // Both are bound by HBM: every element is read and written once (16384 x 4096 bf16 with residual, y
-// and checkpoint: 95 us, 6.3 TB/s; the gradient with dh: 85 us, 6.3 TB/s; plain loads and stores of
-// the same bytes take 94 and 78 us). A row belongs to `tpr` threads (a multiple of 32) that hold it
+// and checkpoint: 95 us on fixed buffers, 6.3 TB/s; the gradient with dh: 85 us, 6.3 TB/s; plain loads
+// and stores of the same bytes take 94 and 78 us). Not so unaligned rows (8000 x 4093: 143 and 84 us,
+// floors 45 and 40), whose outputs leave one element at a time, rows over 8192 columns (4096 x 14336: 164
+// and 322, floors 81 and 72), which come without copies ahead and in the gradient twice, and narrow rows,
+// of which a warp holds one (131072 x 128: 47 and 57, floors 23 and 21; half of its lanes idle). A row belongs to `tpr` threads (a multiple of 32) that hold it
 // in registers, VPT accesses of V elements each: V = 8 (16-byte accesses) when every row is aligned
 // to eight elements, V = 1 otherwise, where a warp reads 32 consecutive elements per access. In both,
 // a 32-element checkpoint block lies within a warp: four lanes of one access (V = 8) or all 32 (V = 1).

@@ -14,7 +14,9 @@ Any other, and any that is refused, takes the path below through ctypes. Inputs
 are CUDA tensors whose last dimension is contiguous (rows may be strided); leading dimensions are
 taken as rows. Outputs and workspaces come from torch's allocator on the stream the call runs on
 (`stream`, or the current stream of the tensors' device), so calls on several streams, and calls
-captured into several graphs, share nothing.
+captured into several graphs, share nothing. Inputs that belong to another stream are the caller's to
+keep until the call's work is done. Nothing is recorded for autograd: outputs are detached, and the
+caller calls the backward operators.
 """
 from __future__ import annotations
 
